@@ -48,6 +48,7 @@ EXPORTS = (
     "xkv_selftest_expired_wait",
     "xkv_full_reconstruct",
     "xkv_dense_workspace_size", "xkv_dense_attention_decode",
+    "xkv_kv8_append", "xkv_kv8_workspace_size", "xkv_kv8_attention_decode", "xkv_kv8_evict",
     "xkv_ner_workspace_size", "xkv_ner", "xkv_energy_rank",
 )
 
@@ -87,6 +88,18 @@ class DenseParams(C.Structure):
     """Mirror of xkv_dense_params."""
     _fields_ = [("batch", C.c_int), ("n_q_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
                 ("T", C.c_int64), ("dtype", C.c_int)]
+
+
+class KV8Params(C.Structure):
+    """Mirror of xkv_kv8_params."""
+    _fields_ = [("batch", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("block", C.c_int),
+                ("capacity", C.c_int64)]
+
+
+class KV8Pointers(C.Structure):
+    """Mirror of xkv_kv8_cache."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("weight", C.c_void_p), ("ids", C.c_void_p)]
 
 
 def _load():
@@ -139,6 +152,13 @@ def _load():
                                            C.c_int, vp, vp]),
         "xkv_dense_workspace_size": (C.c_int, [C.POINTER(DenseParams), C.POINTER(sz)]),
         "xkv_dense_attention_decode": (C.c_int, [C.POINTER(DenseParams), vp, vp, vp, vp, vp, sz, vp]),
+        "xkv_kv8_append": (C.c_int, [C.POINTER(KV8Params), C.POINTER(KV8Pointers), vp, vp, i64, C.c_int, vp, vp, i64,
+                                     i64, vp]),
+        "xkv_kv8_workspace_size": (C.c_int, [C.POINTER(KV8Params), C.c_int, C.POINTER(sz)]),
+        "xkv_kv8_attention_decode": (C.c_int, [C.POINTER(KV8Params), C.POINTER(KV8Pointers), vp, C.c_int, C.c_int, vp,
+                                               vp, C.c_int, vp, sz, vp]),
+        "xkv_kv8_evict": (C.c_int, [C.POINTER(KV8Params), C.POINTER(KV8Pointers), vp, C.c_int, C.c_int, C.c_int, vp,
+                                    vp]),
         "xkv_ner_workspace_size": (C.c_int, [C.c_int, C.c_int, C.POINTER(sz)]),
         "xkv_ner": (C.c_int, [vp, C.c_int, C.c_int, C.c_double, vp, vp, vp, vp, sz, vp]),
         "xkv_energy_rank": (C.c_int, [vp, C.c_int, C.c_int, C.c_double, vp, vp, vp, sz, vp]),
@@ -430,6 +450,111 @@ def xkv_dense_attention_decode(p: DenseParams, q, K, V, out, ws=None, stream=Non
     ws = ws if ws is not None else workspace(xkv_dense_workspace_size(p), q.device)
     _check(lib.xkv_dense_attention_decode(C.byref(p), _ptr(q), _ptr(K), _ptr(V), _ptr(out), _ptr(ws), ws.numel(),
                                           _stream(stream)), "xkv_dense_attention_decode")
+
+
+# ------------------------------------------------------- 8-bit KV cache
+def kv8_params(batch, n_kv_heads, head_dim, block, capacity) -> KV8Params:
+    return KV8Params(batch, n_kv_heads, head_dim, block, capacity)
+
+
+class KV8Cache:
+    """One layer's 8-bit KV cache: k, v [B][Hkv][capacity][hd] float8_e4m3fn, k_scale, v_scale
+    [B][Hkv][capacity / block] f32 and, for eviction, weight (f32) and ids (int32) of the same
+    shape as the scales.  The tensors stay the caller's; the object keeps them alive."""
+
+    def __init__(self, k, v, k_scale, v_scale, weight=None, ids=None):
+        for t, dt in ((k, torch.float8_e4m3fn), (v, torch.float8_e4m3fn), (k_scale, torch.float32),
+                      (v_scale, torch.float32), (weight, torch.float32), (ids, torch.int32)):
+            if t is None:
+                continue
+            if t.dtype != dt or t.dim() != (4 if dt == torch.float8_e4m3fn else 3):
+                raise ValueError("k, v are 4-d float8_e4m3fn; scales and weight 3-d float32, ids 3-d int32")
+            if t.device != k.device:
+                raise ValueError("the tensors of a cache must be on one device")
+        if v.shape != k.shape or k_scale.shape[:2] != k.shape[:2] or k_scale.shape[2] == 0 or \
+                k.shape[2] % k_scale.shape[2] != 0:
+            raise ValueError("k and v need one shape, and scales [B][Hkv][capacity / block]")
+        for t in (v_scale, weight, ids):
+            if t is not None and t.shape != k_scale.shape:
+                raise ValueError("scales, weight and ids need one shape")
+        self.k, self.v, self.k_scale, self.v_scale, self.weight, self.ids = k, v, k_scale, v_scale, weight, ids
+        self.device = k.device
+        self.pointers = KV8Pointers(*(_ptr(t) for t in (k, v, k_scale, v_scale, weight, ids)))
+
+    @classmethod
+    def empty(cls, p: KV8Params, device=None):
+        """Room for p.capacity rows of every (sequence, KV head), with weight and ids."""
+        device = device or "cuda"
+        nblk = (p.batch, p.n_kv_heads, p.capacity // p.block)
+        rows = (p.batch, p.n_kv_heads, p.capacity, p.head_dim)
+        return cls(torch.empty(rows, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(rows, dtype=torch.float8_e4m3fn, device=device),
+                   *(torch.empty(nblk, dtype=torch.float32, device=device) for _ in range(3)),
+                   torch.empty(nblk, dtype=torch.int32, device=device))
+
+
+def _kv8_check(p: KV8Params, cache: KV8Cache, lens, *tensors):
+    """Shapes that the C call cannot see: the cache is p's, lens and the other [B] arrays are
+    int32, and everything lies on the current device."""
+    if tuple(cache.k.shape) != (p.batch, p.n_kv_heads, p.capacity, p.head_dim) or \
+            cache.k_scale.shape[2] * p.block != p.capacity:
+        raise ValueError("the cache's tensors do not have p's sizes")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache is not on the current CUDA device")
+    for t in (lens, *tensors):
+        if t is not None and t.device != cache.device:
+            raise ValueError("all tensors must be on the cache's device")
+
+
+def _lens_ptr(p: KV8Params, t):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != p.batch or not t.is_contiguous():
+        raise ValueError("lengths and counts are contiguous int32 tensors of one entry per sequence")
+    return t.data_ptr()
+
+
+def xkv_kv8_append(p: KV8Params, cache: KV8Cache, lens, k_new, v_new, counts=None, stream=None):
+    """Round new rows k_new, v_new [B][n][Hkv hd] (views with contiguous rows are accepted) into the
+    cache at positions lens[b] ...; counts[b] <= n rows where given.  lens is not advanced."""
+    _kv8_check(p, cache, lens, k_new, v_new, counts)
+    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype or \
+            k_new.shape[0] != p.batch or k_new.shape[2] != p.n_kv_heads * p.head_dim:
+        raise ValueError("k_new and v_new are [B][n][Hkv hd] of one dtype")
+    n = k_new.shape[1]
+    if k_new.stride(2) != 1 or (k_new.stride() != v_new.stride()):
+        raise ValueError("k_new and v_new need contiguous rows and the same strides")
+    ld = k_new.stride(1) if n > 1 else max(k_new.stride(1), k_new.shape[2])
+    _check(lib.xkv_kv8_append(p, cache.pointers, _lens_ptr(p, lens), _lens_ptr(p, counts), n,
+                              dtype_code(k_new.dtype), k_new.data_ptr(), v_new.data_ptr(), ld,
+                              k_new.stride(0) if p.batch > 1 else 0, _stream(stream)), "xkv_kv8_append")
+
+
+def xkv_kv8_workspace_size(p: KV8Params, n_q_heads: int) -> int:
+    return _wsize(lib.xkv_kv8_workspace_size, C.byref(p), n_q_heads)
+
+
+def xkv_kv8_attention_decode(p: KV8Params, cache: KV8Cache, lens, q, out, accumulate: bool = False, ws=None,
+                             stream=None):
+    """One decode step over the 8-bit cache; writes out [B][Hq][hd] f32 and, with accumulate, adds
+    every block's attention weight to cache.weight."""
+    _kv8_check(p, cache, lens, q, out, ws)
+    if q.dim() != 3 or q.shape[0] != p.batch or q.shape[2] != p.head_dim or out.shape != q.shape or \
+            out.dtype != torch.float32:
+        raise ValueError("q is [B][Hq][hd] and out the same shape in float32")
+    n_q_heads = q.shape[1]
+    ws = ws if ws is not None else workspace(xkv_kv8_workspace_size(p, n_q_heads), q.device)
+    _check(lib.xkv_kv8_attention_decode(p, cache.pointers, _lens_ptr(p, lens), n_q_heads, dtype_code(q.dtype), _ptr(q),
+                                        _ptr(out), int(bool(accumulate)), _ptr(ws), ws.numel() * ws.element_size(),
+                                        _stream(stream)), "xkv_kv8_attention_decode")
+
+
+def xkv_kv8_evict(p: KV8Params, cache: KV8Cache, lens, budget: int, sink: int, recent: int, lens_out, stream=None):
+    """Keep `budget` blocks of every longer sequence and KV head: the first `sink`, the newest
+    `recent` and those with the most weight.  lens_out receives the lengths after it."""
+    _kv8_check(p, cache, lens, lens_out)
+    _check(lib.xkv_kv8_evict(p, cache.pointers, _lens_ptr(p, lens), budget, sink, recent, _lens_ptr(p, lens_out),
+                             _stream(stream)), "xkv_kv8_evict")
 
 
 # -------------------------------------------------------------------- NER

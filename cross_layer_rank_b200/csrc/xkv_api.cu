@@ -164,7 +164,7 @@ const char* xkv_status_string(xkv_status s) {
   return "unknown status";
 }
 
-int xkv_version(void) { return (1 << 16) | 0; }
+int xkv_version(void) { return (1 << 16) | 1; }
 
 // Takes the status word out and leaves 0 in one atomic step, so that a code
 // recorded by a kernel on another stream is either returned now or kept for
@@ -703,6 +703,86 @@ xkv_status xkv_dense_attention_decode(const xkv_dense_params* p, const void* q, 
     return XKV_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < dense_workspace(p) || !aligned256(workspace)) return XKV_ERR_WORKSPACE;
   return dense_launch(p, q, K, V, out, workspace, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------- 8-bit KV cache
+static inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static xkv_status check_kv8(const xkv_kv8_params* p) {
+  if (!p || p->batch < 1 || p->n_kv_heads < 1 || p->head_dim < 1 || p->block < 1 || p->capacity < p->block ||
+      p->capacity % p->block != 0)
+    return XKV_ERR_INVALID_ARG;
+  if (p->head_dim % 16 != 0 || p->head_dim > 256) return XKV_ERR_UNSUPPORTED;
+  if (p->block < 8 || p->block > 128 || (p->block & (p->block - 1)) != 0) return XKV_ERR_UNSUPPORTED;
+  const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads, most = int64_t(1) << 30;
+  if (p->capacity > most || units > most || units * ((p->capacity + 127) / 128) > most) return XKV_ERR_UNSUPPORTED;
+  return XKV_OK;
+}
+
+static xkv_status check_kv8_cache(const xkv_kv8_cache* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !aligned16(c->k) || !aligned16(c->v) ||
+      !aligned4(c->k_scale) || !aligned4(c->v_scale) || !aligned4(c->weight) || !aligned4(c->ids))
+    return XKV_ERR_INVALID_ARG;
+  return XKV_OK;
+}
+
+xkv_status xkv_kv8_append(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
+                          const int32_t* counts, int64_t n_new, xkv_dtype dtype, const void* k_new, const void* v_new,
+                          int64_t row_stride, int64_t batch_stride, void* stream) {
+  xkv_status s = check_kv8(p);
+  if (s == XKV_OK) s = check_kv8_cache(cache);
+  if (s != XKV_OK) return s;
+  if (dtype != XKV_F32 && dtype != XKV_BF16) return XKV_ERR_INVALID_ARG;
+  const int per16 = dtype == XKV_BF16 ? 8 : 4;
+  if (!lens || !aligned4(lens) || !aligned4(counts) || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) ||
+      n_new < 0 || n_new > p->capacity || row_stride < static_cast<int64_t>(p->n_kv_heads) * p->head_dim ||
+      row_stride % per16 != 0 || batch_stride < 0 || batch_stride % per16 != 0)
+    return XKV_ERR_INVALID_ARG;
+  if (n_new == 0) return XKV_OK;
+  return kv8_append_launch(p, cache, lens, counts, n_new, dtype, k_new, v_new, row_stride, batch_stride,
+                           static_cast<cudaStream_t>(stream));
+}
+
+static xkv_status check_kv8_heads(const xkv_kv8_params* p, int n_q_heads) {
+  const xkv_status s = check_kv8(p);
+  if (s != XKV_OK) return s;
+  if (n_q_heads < 1 || n_q_heads % p->n_kv_heads != 0) return XKV_ERR_INVALID_ARG;
+  return n_q_heads / p->n_kv_heads > 16 ? XKV_ERR_UNSUPPORTED : XKV_OK;
+}
+
+xkv_status xkv_kv8_workspace_size(const xkv_kv8_params* p, int n_q_heads, size_t* bytes) {
+  if (!bytes) return XKV_ERR_INVALID_ARG;
+  const xkv_status s = check_kv8_heads(p, n_q_heads);
+  if (s != XKV_OK) return s;
+  *bytes = kv8_plan(p, n_q_heads).bytes;
+  return XKV_OK;
+}
+
+xkv_status xkv_kv8_attention_decode(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
+                                    int n_q_heads, xkv_dtype dtype, const void* q, float* out, int accumulate,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  xkv_status s = check_kv8_heads(p, n_q_heads);
+  if (s == XKV_OK) s = check_kv8_cache(cache);
+  if (s != XKV_OK) return s;
+  if ((dtype != XKV_F32 && dtype != XKV_BF16) || !lens || !aligned4(lens) || !q || !out || !aligned16(q) ||
+      !aligned16(out) || (accumulate && !cache->weight))
+    return XKV_ERR_INVALID_ARG;
+  const KV8Plan plan = kv8_plan(p, n_q_heads);
+  if (!workspace || ws_bytes < plan.bytes || !aligned256(workspace)) return XKV_ERR_WORKSPACE;
+  return kv8_attend_launch(p, cache, lens, n_q_heads, dtype, q, out, accumulate, plan, workspace,
+                           static_cast<cudaStream_t>(stream));
+}
+
+xkv_status xkv_kv8_evict(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens, int budget, int sink,
+                         int recent, int32_t* lens_out, void* stream) {
+  xkv_status s = check_kv8(p);
+  if (s == XKV_OK) s = check_kv8_cache(cache);
+  if (s != XKV_OK) return s;
+  if (!cache->weight || !cache->ids || !lens || !aligned4(lens) || !lens_out || !aligned4(lens_out) || recent < 1 ||
+      sink < 0 || budget < 1 || static_cast<int64_t>(sink) + recent > budget)
+    return XKV_ERR_INVALID_ARG;
+  if (lens_out < lens + p->batch && lens < lens_out + p->batch) return XKV_ERR_INVALID_ARG;
+  return kv8_evict_launch(p, cache, lens, budget, sink, recent, lens_out, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------- NER

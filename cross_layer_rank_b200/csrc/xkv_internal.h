@@ -99,6 +99,22 @@ xkv_status compress_launch(const CompressPlan& plan, const void* const* X, int G
                            int64_t ldx, xkv_dtype dt, int iters, uint64_t seed, void* A, void* Bt,
                            float* eigvals, float* gram_out, void* ws, cudaStream_t st);
 
+// ------------------------------------------------------- 8-bit KV cache
+struct KV8Plan {
+  int ctas;  // attention CTAs (shares of the tiles)
+  int64_t tiles_cap;
+  size_t off_wpart, off_wref, bytes;
+};
+KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads);
+xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens,
+                             const int32_t* counts, int64_t n_new, xkv_dtype dt, const void* k_new, const void* v_new,
+                             int64_t row_stride, int64_t batch_stride, cudaStream_t st);
+xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens, int n_q_heads,
+                             xkv_dtype dt, const void* q, float* out, int accumulate, const KV8Plan& plan, void* ws,
+                             cudaStream_t st);
+xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens, int budget, int sink,
+                            int recent, int32_t* lens_out, cudaStream_t st);
+
 // ---------------------------------------------------- multi-step decode
 size_t append_workspace(const xkv_append_params* p);
 xkv_status append_launch(const xkv_append_params* p, const void* const* k_new, const void* const* v_new,

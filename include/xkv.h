@@ -417,6 +417,88 @@ XKV_API xkv_status xkv_dense_attention_decode(const xkv_dense_params* p, const v
                                       const void* V, float* out, void* workspace, size_t ws_bytes,
                                       void* stream);
 
+/* ------------------------------------------------------ 8-bit KV cache */
+/* A whole (not low-rank) KV cache of one layer held in 8 bits, beside the
+ * compressed caches above and the full one of xkv_dense_attention_decode: the
+ * decode attention of [KQ-SVD] 3.2 over it, with post-RoPE keys (as there), and
+ * eviction of the blocks that attention has used least.  The pages have no
+ * counterpart to the number format or to the eviction rule; both are stated here.
+ *
+ *   k, v             : [B][Hkv][capacity][hd] e4m3 codes (one byte each).
+ *   k_scale, v_scale : [B][Hkv][capacity / block] f32, one scale per block of
+ *                      `block` token rows and KV head, a power of two:
+ *                      2^e with the least e >= -117 for which every finite value
+ *                      of the block is within 448 * 2^e.  Row t stands for
+ *                      code * scale[t / block].
+ *   weight           : [B][Hkv][capacity / block] f32, the attention weight that
+ *                      each block has been given so far; NULL without eviction.
+ *   ids              : [B][Hkv][capacity / block] int32, the number of the block
+ *                      in the sequence (0, 1, ...; blocks change slots when others
+ *                      are evicted); NULL without eviction.
+ * Lengths are on the device: lens [B] int32 holds the tokens of every sequence,
+ * the same for all its heads; the calls read it and never write it, so that one
+ * array serves every layer and the caller advances it once a step.  What stands
+ * behind a sequence's last row is neither read nor written.  A length outside
+ * [0, capacity] is taken as the nearer end and XKV_ERR_INVALID_ARG is recorded
+ * in the device status word.
+ * head_dim is a multiple of 16 up to 256; block is 8, 16, 32, 64 or 128 and
+ * divides capacity; B Hkv ceil(capacity / 128) <= 2^30 (else
+ * XKV_ERR_UNSUPPORTED).  k and v are 16-byte aligned; the arrays of scales,
+ * weights, ids and lengths need only their elements' 4 bytes. */
+typedef struct xkv_kv8_params {
+  int batch, n_kv_heads, head_dim;
+  int block;        /* tokens per scale */
+  int64_t capacity; /* token rows per (sequence, KV head) */
+} xkv_kv8_params;
+typedef struct xkv_kv8_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  float* weight;
+  int32_t* ids;
+} xkv_kv8_cache;
+
+/* Appends rows to every sequence: counts[b] of them (n_new where counts is
+ * NULL; 0 <= counts[b] <= n_new) from k_new, v_new [B][n_new][Hkv hd] in
+ * `dtype`, with `row_stride` and `batch_stride` elements between rows and
+ * sequences (each row_stride a multiple of 16 bytes), at positions lens[b] ....
+ * Codes are the nearest e4m3 numbers (ties to even) of value / scale; an
+ * infinite value becomes the largest code, a NaN stays NaN, and neither counts
+ * for the scale.  A block that held rows before keeps the larger of its scale
+ * and the new rows' one; when that makes its scale grow, its codes are rounded
+ * once more on the new scale.  A block opened by the call gets weight 0 and the
+ * number after the last block's.  Rows past the capacity are dropped and
+ * XKV_ERR_INVALID_ARG is recorded in the device status word.  lens is not
+ * advanced. */
+XKV_API xkv_status xkv_kv8_append(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
+                                  const int32_t* counts, int64_t n_new, xkv_dtype dtype, const void* k_new,
+                                  const void* v_new, int64_t row_stride, int64_t batch_stride, void* stream);
+
+/* One decode step over the cache:  o_g = softmax(q_g K^T / sqrt(hd)) V over the
+ * lens[b] rows of the query head's KV head; 0 where a sequence has none.
+ *   q   : [B][Hq][hd] in `dtype`, Hq a multiple of n_kv_heads, Hq / Hkv <= 16
+ *         (else XKV_ERR_UNSUPPORTED).   out : [B][Hq][hd] f32.
+ * With accumulate, every block's weight grows by the softmax probabilities of
+ * its rows, summed over the KV head's query heads.  A step gives the same bits
+ * whenever it is repeated. */
+XKV_API xkv_status xkv_kv8_workspace_size(const xkv_kv8_params* p, int n_q_heads, size_t* bytes);
+XKV_API xkv_status xkv_kv8_attention_decode(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
+                                            int n_q_heads, xkv_dtype dtype, const void* q, float* out,
+                                            int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* Cuts every sequence of more than `budget` blocks down to `budget`, for each KV
+ * head on its own: the blocks with ids below `sink` and the `recent` newest ones
+ * stay, and of the others those with the most weight (ties to the lower slot; a
+ * NaN counts below every number).  In place: kept blocks in slots below budget - 1
+ * stay where they are; the others move, in order, into the slots that are free,
+ * the newest block (the only one that may be part-filled) into slot budget - 1.
+ * Softmax does not depend on the order of rows.  lens_out[b] is the length
+ * after it, lens[b] - (n - budget) block for n = ceil(lens[b] / block) > budget;
+ * lens_out may not overlap lens.
+ * Requires 1 <= recent, 0 <= sink, sink + recent <= budget, weight and ids; at
+ * most 131072 blocks per sequence (else XKV_ERR_UNSUPPORTED). */
+XKV_API xkv_status xkv_kv8_evict(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens, int budget,
+                                 int sink, int recent, int32_t* lens_out, void* stream);
+
 /* ------------------------------------------------------------------ NER */
 /* [KV-CoRE] 2.B per diagonal block C_ll (block x block) of an n x n f32 Gram:
  * eigenvalues lambda, numerical rank r = #{lambda_i > rank_rel_tol lambda_max},
