@@ -260,146 +260,446 @@ __device__ inline Line walk_line(const AttendArgs& a, int b0, int x) {
   return r;
 }
 
-// A simple form: one thread per token row for the scores, one per column for
-// the values.
+// One role's position in its CTA's share: tile t of unit (b, h).
+struct Walk {
+  int b, h, t, nt;
+  int64_t len;
+  __device__ __forceinline__ void load(const AttendArgs& a) {
+    len = checked_len(a.lens[b], a.capacity, nullptr);
+    nt = static_cast<int>((len + kTile - 1) / kTile);
+  }
+  __device__ __forceinline__ Walk(const AttendArgs& a, int first_b, int skip) : b(first_b) {
+    load(a);
+    h = skip / nt;
+    t = skip % nt;
+  }
+  // The next tile; only where there is one.
+  __device__ __forceinline__ void step(const AttendArgs& a) {
+    if (++t < nt) return;
+    t = 0;
+    if (++h < a.Hkv) return;
+    h = 0;
+    do {
+      ++b;
+      load(a);
+    } while (nt == 0);
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float redux_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Offset of byte `c` of row `r` in a tile of 128-byte rows under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) {
+  return r * 128u + ((((c >> 4) ^ r) & 7u) << 4) + (c & 15u);
+}
+
+// A number as a sum of e4m3 pieces: x = sum_i 16^-i piece_i.  Each piece holds
+// four significant bits and leaves a remainder of at most 2^-4 of its own, exact
+// in f32, so two pieces hold a bf16 number, six an f32 one, and five a
+// probability to 2^-20 of itself.  Numbers below 2^-6 of the first piece's scale
+// run out of exponents instead: they are held to 2^-10 16^-(pieces - 1).
+constexpr int kPiecesP = 5;
 template <typename T>
-__global__ void __launch_bounds__(128) kv8_attend_kernel(const AttendArgs a) {
-  extern __shared__ float sm[];
-  __shared__ Line s_line;
-  __shared__ int s_total;
-  __shared__ float s_red[4][16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = a.gq, hd = a.hd;
-  float* qs = sm;              // [gq][hd]
-  float* ps = qs + gq * hd;    // [gq][128]
+struct Pieces;
+template <>
+struct Pieces<__nv_bfloat16> {
+  static constexpr int n = 2;
+};
+template <>
+struct Pieces<float> {
+  static constexpr int n = 6;
+};
+
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpQ = 10, kAttendThreads = 384;  // warps 0-7: softmax, two warpgroups
+constexpr int kMaxStages = 8;
+constexpr int kAtom = kTile * 128;  // bytes of 128 rows x 128 columns
+
+template <typename T, int GQ, int HDA>
+struct AttendShape {
+  static constexpr int nq = Pieces<T>::n * GQ, np = kPiecesP * GQ;          // operand rows in use
+  static constexpr int ns = (nq + 15) / 16 * 16, no = (np + 15) / 16 * 16;  // and MMA widths
+  static constexpr int tmem_used = 2 * ns + 2 * HDA * no;
+  static constexpr int tmem = tmem_used <= 64 ? 64 : tmem_used <= 128 ? 128 : tmem_used <= 256 ? 256 : 512;
+  static constexpr int bytes_p = 2 * no * 128, bytes_q = 2 * HDA * ns * 128;
+  static_assert(tmem_used <= 512, "TMEM columns");
+  static constexpr int stages() {
+    const int s = (227 * 1024 - 4096 - 1024 - bytes_p - bytes_q) / (2 * HDA * kAtom);
+    return s < kMaxStages ? s : kMaxStages;
+  }
+  static constexpr int smem() { return stages() * 2 * HDA * kAtom + bytes_p + bytes_q + 1024; }
+};
+
+// Decode attention on the tensor cores.  For a tile of 128 token rows
+//   S = K Q^T   (128 rows x pieces of the group's queries, K = head_dim),
+//   O = V^T P^T (128 columns x pieces of the probabilities, K = 128 rows):
+// the codes go from HBM to the MMA as they are (TMA, 128-byte swizzle), nothing
+// is unpacked, and the small operands carry their precision in e4m3 pieces
+// instead.  A block's scale enters as a factor of S's row or of P's column.
+//   warps 0-3, 4-7: softmax of tiles in turn; thread = token row of S, then
+//                   column of O, which is summed in f32 registers;
+//   warp 8: TMA of K and V rings; warp 9: MMA; warps 10-11: queries' pieces.
+// Rows behind the sequence's end are masked in S, and their V rows zeroed before
+// the MMA (0 * NaN).
+template <typename T, int GQ, int HDA>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const AttendArgs a) {
+  using Sh = AttendShape<T, GQ, HDA>;
+  constexpr int kStages = Sh::stages(), kNq = Pieces<T>::n;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_total, s_before, s_b;
+  __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
+  __shared__ float s_sum[2][4][GQ], s_qc[2][GQ];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sk = sm;
+  uint8_t* sv = sk + kStages * HDA * kAtom;
+  uint8_t* sp = sv + kStages * HDA * kAtom;
+  uint8_t* sq = sp + Sh::bytes_p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&q_full[i], 64);
+      mbar_init(&q_empty[i], 1 + 256);
+    }
+    mbar_init(&done, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&s_tmem, Sh::tmem);
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
   if (warp == 0) {
     Line l = walk_line(a, 0, -1);
-    const Share s = share_of(l.total, a.ctas, blockIdx.x);
     const int total = l.total;
+    const Share s = share_of(total, a.ctas, blockIdx.x);
     if (s.lo < s.hi) l = walk_line(a, 0, s.lo);
     if (lane == 0) {
-      s_line = l;
       s_total = total;
+      s_before = l.before;
+      s_b = l.b;
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const Share sh = share_of(s_total, a.ctas, blockIdx.x);
-  if (sh.lo >= sh.hi) return;
-  int b = s_line.b, nt = tiles_of(a, b);
-  int h = (sh.lo - s_line.before) / nt, t = (sh.lo - s_line.before) % nt;
-  const float c0 = kLog2e / sqrtf(static_cast<float>(hd));
-  const int64_t nblk = a.capacity / a.block;
-  for (int x = sh.lo; x < sh.hi;) {
-    // one unit's run of tiles
-    const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
-    const int64_t len = checked_len(a.lens[b], a.capacity, nullptr);
-    const int t1 = min(nt, t + sh.hi - x);
-    const int n_run = t1 - t;
-    __syncthreads();
-    for (int i = tid; i < gq * hd; i += 128)
-      qs[i] = to_f(static_cast<const T*>(a.q)[(static_cast<int64_t>(b) * a.Hkv + h) * gq * hd + i]);
-    float acc[2][16], m[16], l[16];
-#pragma unroll
-    for (int g = 0; g < 16; ++g) {
-      acc[0][g] = acc[1][g] = l[g] = 0.f;
-      m[g] = -INFINITY;
-    }
-    for (; t < t1; ++t) {
-      __syncthreads();
-      const int64_t row = static_cast<int64_t>(t) * kTile + tid;
-      float s[16];
-#pragma unroll
-      for (int g = 0; g < 16; ++g) s[g] = 0.f;
-      const bool live = row < len;
-      if (live) {
-        const uint8_t* kr = a.k + (unit * a.capacity + row) * hd;
-        for (int j = 0; j < hd; j += 16) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kr + j);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = from_e4m3x2(static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))));
-#pragma unroll
-            for (int g = 0; g < 16; ++g)
-              if (g < gq) s[g] = fmaf(f.x, qs[g * hd + j + 2 * e], fmaf(f.y, qs[g * hd + j + 2 * e + 1], s[g]));
+  const int n = sh.hi - sh.lo;
+  // A wait that runs out sets s_abort, after which no wait waits: the TMA and MMA
+  // warps stop, the others run through their loops and meet every barrier.
+  volatile int* abort = &s_abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*abort) return false;
+    if (mbar_wait(bar, parity, a.status)) return true;
+    *abort = 1;
+    return false;
+  };
+  if (n > 0) {
+    Walk w(a, s_b, sh.lo - s_before);
+    if (warp == kWarpTma) {
+      if (lane == 0) {
+        int i = 0;
+        for (; i < n; ++i) {
+          const int st = i % kStages;
+          const uint32_t ph = ((i / kStages) & 1) ^ 1;
+          const int unit = w.b * a.Hkv + w.h;
+          if (i >= kStages && !wait(&k_empty[st], ph)) break;
+          mbar_arrive_expect_tx(&k_full[st], HDA * kAtom);
+          for (int x = 0; x < HDA; ++x)
+            tma_load_3d(sk + (st * HDA + x) * kAtom, &map_k, &k_full[st], 128 * x, w.t * kTile, unit);
+          if (i >= kStages && !wait(&v_empty[st], ph)) {
+            drain_ring(k_full, kStages, i + 1, a.status);
+            drain_ring(v_full, kStages, i, a.status);
+            i = -1;
+            break;
           }
+          mbar_arrive_expect_tx(&v_full[st], HDA * kAtom);
+          for (int x = 0; x < HDA; ++x)
+            tma_load_3d(sv + (st * HDA + x) * kAtom, &map_v, &v_full[st], 128 * x, w.t * kTile, unit);
+          if (i + 1 < n) w.step(a);
         }
-        const float c = c0 * a.k_scale[unit * nblk + row / a.block];
-#pragma unroll
-        for (int g = 0; g < 16; ++g) s[g] *= c;
+        if (i >= 0 && i < n) {
+          drain_ring(k_full, kStages, i, a.status);
+          drain_ring(v_full, kStages, i, a.status);
+        }
       }
-#pragma unroll
-      for (int g = 0; g < 16; ++g) {
-        const float w = warp_max(live ? s[g] : -INFINITY);
-        if (lane == 0) s_red[warp][g] = w;
+    } else if (warp == kWarpMma) {
+      if (lane == 0) {
+        constexpr uint32_t id_s = umma_idesc_e4m3(128, Sh::ns), id_o = umma_idesc_e4m3(128, Sh::no, true, false);
+        const int ksteps = (a.hd + 31) / 32;
+        int seg = 0;  // the unit whose S comes next
+        auto issue_s = [&](int i) {
+          const int st = i % kStages, wg = i & 1, qb = seg & 1;
+          if (i == 0 || w.t == 0) {
+            if (!wait(&q_full[qb], (seg >> 1) & 1)) return false;
+          }
+          if (!wait(&k_full[st], (i / kStages) & 1)) return false;
+          tc_fence_after();
+          for (int s = 0; s < ksteps; ++s) {
+            const int x = s / 4, o = (s % 4) * 32;
+            umma_e4m3(tmem + wg * Sh::ns, umma_desc_sw128(smem_u32(sk + (st * HDA + x) * kAtom) + o),
+                      umma_desc_sw128(smem_u32(sq + (qb * HDA + x) * Sh::ns * 128) + o), id_s, s > 0);
+          }
+          umma_commit(&s_full[wg]);
+          umma_commit(&k_empty[st]);
+          if (w.t == w.nt - 1 || i == n - 1) {
+            umma_commit(&q_empty[qb]);
+            ++seg;
+          }
+          if (i + 1 < n) w.step(a);
+          return true;
+        };
+        bool ok = issue_s(0);
+        if (ok && n > 1) ok = issue_s(1);
+        for (int i = 0; ok && i < n; ++i) {
+          const int st = i % kStages, wg = i & 1;
+          ok = wait(&v_full[st], (i / kStages) & 1) && wait(&p_full[wg], (i >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          for (int x = 0; x < HDA; ++x)
+            for (int s = 0; s < 4; ++s)
+              umma_e4m3(tmem + 2 * Sh::ns + (wg * HDA + x) * Sh::no,
+                        umma_desc_sw128_mn(smem_u32(sv + (st * HDA + x) * kAtom) + s * 4096, kAtom, 1024),
+                        umma_desc_sw128(smem_u32(sp + wg * Sh::no * 128) + s * 32), id_o, s > 0);
+          umma_commit(&o_full[wg]);
+          umma_commit(&v_empty[st]);
+          if (i + 2 < n) ok = issue_s(i + 2);
+        }
+        umma_commit(&done);  // what was issued ends before the CTA's memory goes
+        (void)mbar_wait(&done, 0, a.status);
       }
-      __syncthreads();
-      float* wp = a.wpart ? a.wpart + (unit * a.tiles_cap + t) * (kTile / sub_rows(a.block)) * gq : nullptr;
+    } else if (warp >= kWarpQ) {
+      // queries of one unit: pieces, K-major rows piece * GQ + g, zero past head_dim and past the group
+      int seg = 0;
+      for (int i = 0; i < n;) {
+        const int qb = seg & 1;
+        if (seg >= 2) (void)wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1);
+        const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+        for (int g = warp - kWarpQ; g < GQ; g += 2) {
+          const T* q = static_cast<const T*>(a.q) + (unit * a.gq + g) * a.hd;
+          float x[4 * HDA];
+          uint32_t big = 0;
+#pragma unroll
+          for (int k = 0; k < 4 * HDA; ++k) {
+            const int j = k * 32 + lane;
+            x[k] = g < a.gq && j < a.hd ? to_f(q[j]) : 0.f;
+            const uint32_t m = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+            big = max(big, m < 0x7F800000u ? m : 0u);
+          }
+          const int e = scale_exp(__reduce_max_sync(0xffffffffu, big));
+          const float inv = pow2f(-e);
+#pragma unroll
+          for (int k = 0; k < 4 * HDA; ++k) {
+            const int j = k * 32 + lane;
+            // what is not finite makes the head's logits NaN
+            float r = (__float_as_uint(x[k]) & 0x7FFFFFFFu) < 0x7F800000u ? x[k] * inv : __uint_as_float(0x7FC00000u);
+#pragma unroll
+            for (int p = 0; p < kNq; ++p) {
+              const uint16_t c = to_e4m3x2(r, 0.f);
+              r = 16.f * (r - from_e4m3x2(c).x);
+              sq[(qb * HDA + (j >> 7)) * Sh::ns * 128 + swz128(p * GQ + g, j & 127)] = static_cast<uint8_t>(c);
+            }
+          }
+          if (lane == 0) s_qc[qb][g] = pow2f(e) * (kLog2e / sqrtf(static_cast<float>(a.hd)));
+        }
+        fence_proxy_async();
+        mbar_arrive(&q_full[qb]);
+        ++seg;
+        // to the next unit
+        const int left = w.nt - w.t;
+        i += left;
+        if (i < n) {
+          w.t = w.nt - 1;
+          w.step(a);
+        }
+      }
+    } else {
+      const int wg = warp >> 2, row = tid & 127, quarter = warp & 3;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      const int64_t nblk = a.capacity / a.block;
       const int sub = sub_rows(a.block);
-      const float vs = live ? a.v_scale[unit * nblk + row / a.block] : 0.f;
+      uint8_t* p_op = sp + wg * Sh::no * 128;
+      float acc[HDA][GQ], m[GQ], l[GQ], c[GQ];
+      bool any = false;
+      int seg = 0;
+      for (int i = 0; i < n; ++i) {
+        const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+        if (i == 0 || w.t == 0) {
+          const int qb = seg & 1;
+          (void)wait(&q_full[qb], (seg >> 1) & 1);
 #pragma unroll
-      for (int g = 0; g < 16; ++g) {
-        if (g >= gq) break;
-        const float mt = fmaxf(fmaxf(s_red[0][g], s_red[1][g]), fmaxf(s_red[2][g], s_red[3][g]));
-        const float mn = fmaxf(m[g], mt);
-        const float al = m[g] == mn ? 1.f : exp2f(m[g] - mn);
-        const float p = live ? exp2f(s[g] - mn) : 0.f;
-        m[g] = mn;
-        acc[0][g] *= al;
-        acc[1][g] *= al;
-        l[g] = l[g] * al + p;
-        ps[g * 128 + tid] = live ? p * vs : 0.f;
-        if (wp) {
-          float sum = p;
-          for (int o = 1; o < sub; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (tid % sub == 0) wp[(tid / sub) * gq + g] = sum;
-          if (tid == 0) a.wref[(unit * a.tiles_cap + t) * gq + g] = mn;
+          for (int g = 0; g < GQ; ++g) {
+            c[g] = s_qc[qb][g];
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+#pragma unroll
+            for (int x = 0; x < HDA; ++x) acc[x][g] = 0.f;
+          }
+          mbar_arrive(&q_empty[qb]);
+          any = false;
+          ++seg;
         }
-      }
-      __syncthreads();
-      const int rows = static_cast<int>(min(static_cast<int64_t>(kTile), len - static_cast<int64_t>(t) * kTile));
+        if ((i & 1) == wg) {
+          any = true;
+          const int use = i >> 1, par = use & 1;
+          const int64_t at = static_cast<int64_t>(w.t) * kTile + row;
+          const bool live = at < w.len;
+          const float ks = live ? __ldg(a.k_scale + unit * nblk + at / a.block) : 0.f;
+          const float vs = live ? __ldg(a.v_scale + unit * nblk + at / a.block) : 0.f;
+          float s[GQ];
+          (void)wait(&s_full[wg], par);
+          tc_fence_after();
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const int col = tid + 128 * cc;
-        if (col < hd) {
-          const uint8_t* vr = a.v + (unit * a.capacity + static_cast<int64_t>(t) * kTile) * hd + col;
-          for (int r = 0; r < rows; ++r) {
-            const float vv = from_e4m3x2(vr[static_cast<int64_t>(r) * hd]).x;
+          for (int g = 0; g < GQ; ++g) s[g] = 0.f;
+          constexpr int kCols = Sh::ns <= 48 ? Sh::ns : 48;
 #pragma unroll
-            for (int g = 0; g < 16; ++g)
-              if (g < gq) acc[cc][g] = fmaf(ps[g * 128 + r], vv, acc[cc][g]);
+          for (int k0 = (Sh::ns - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
+            float v[kCols];
+#pragma unroll
+            for (int k = 0; k < kCols; k += 16) tmem_ld16(tmem + lanes + wg * Sh::ns + k0 + k, v + k);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = kCols - 1; k >= 0; --k)
+              if (k0 + k < Sh::nq) s[(k0 + k) % GQ] = fmaf(s[(k0 + k) % GQ], 0.0625f, v[k]);
+          }
+          // The tile's largest logits, and the largest of logit + log2(value scale), which is what a row brings to
+          // O: both as whole numbers, so that every change of reference is an exact power of two.
+          const float ev = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
+          const float vm = live ? __uint_as_float((__float_as_uint(vs) & 0x7FFFFFu) | 0x3F800000u) * 128.f : 0.f;
+#pragma unroll
+          for (int g = 0; g < GQ; ++g) {
+            const float t = live ? s[g] * (c[g] * ks) : -INFINITY;
+            const float t0 = redux_max(t), t1 = redux_max(t + ev);
+            if (lane == 0) {
+              s_max[wg][par][2 * g][quarter] = t0;
+              s_max[wg][par][2 * g + 1][quarter] = t1;
+            }
+          }
+          named_bar_sync(1 + wg, 128);
+          float* wp = a.wpart ? a.wpart + (unit * a.tiles_cap + w.t) * (kTile / sub) * a.gq : nullptr;
+          float back[GQ];
+#pragma unroll
+          for (int g = 0; g < GQ; ++g) {
+            const float4 t0 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * g]);
+            const float4 t1 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * g + 1]);
+            const float mn = fmaxf(m[g], ceilf(fmaxf(fmaxf(t0.x, t0.y), fmaxf(t0.z, t0.w))));
+            const float mv = ceilf(fmaxf(fmaxf(t1.x, t1.y), fmaxf(t1.z, t1.w)));
+            const float al = m[g] == mn ? 1.f : ex2(m[g] - mn);
+            m[g] = mn;
+            back[g] = ex2(mv - mn) * (1.f / 128.f);
+            const float p = live ? ex2(fmaf(s[g], c[g] * ks, -mn)) : 0.f;
+            l[g] = fmaf(l[g], al, p);
+#pragma unroll
+            for (int x = 0; x < HDA; ++x) acc[x][g] *= al;
+            s[g] = live ? ex2(fmaf(s[g], c[g] * ks, ev - mv)) * vm : 0.f;
+            if (wp && g < a.gq) {
+              float sum = p;
+              for (int o = 1; o < sub; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (row % sub == 0) wp[(row / sub) * a.gq + g] = sum;
+              if (row == 0) a.wref[(unit * a.tiles_cap + w.t) * a.gq + g] = mn;
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < kPiecesP; ++p) {
+#pragma unroll
+            for (int g = 0; g < GQ; g += 2) {
+              const uint16_t e = to_e4m3x2(s[g], s[g + 1]);
+              const float2 f = from_e4m3x2(e);
+              s[g] = 16.f * (s[g] - f.x);
+              s[g + 1] = 16.f * (s[g + 1] - f.y);
+              p_op[swz128(p * GQ + g, row)] = static_cast<uint8_t>(e);
+              p_op[swz128(p * GQ + g + 1, row)] = static_cast<uint8_t>(e >> 8);
+            }
+          }
+          if (w.len - static_cast<int64_t>(w.t) * kTile < kTile) {
+            const int st = i % kStages;
+            (void)wait(&v_full[st], (i / kStages) & 1);
+            if (!live) {
+#pragma unroll
+              for (int x = 0; x < HDA; ++x)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  reinterpret_cast<uint4*>(sv + (st * HDA + x) * kAtom + row * 128)[k] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async();
+          tc_fence_before();
+          mbar_arrive(&p_full[wg]);
+          (void)wait(&o_full[wg], par);
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < HDA; ++x) {
+            float sum[GQ];
+#pragma unroll
+            for (int g = 0; g < GQ; ++g) sum[g] = 0.f;
+            // the pieces' columns from the least on, at most 48 registers of them at a time
+            constexpr int kCols = Sh::no <= 48 ? Sh::no : 32;
+#pragma unroll
+            for (int k0 = (Sh::no - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
+              float v[kCols];
+#pragma unroll
+              for (int k = 0; k < kCols; k += 16)
+                if (k0 + k < Sh::no)
+                  tmem_ld16(tmem + lanes + 2 * Sh::ns + (wg * HDA + x) * Sh::no + k0 + k, v + k);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = kCols - 1; k >= 0; --k)
+                if (k0 + k < Sh::np) sum[(k0 + k) % GQ] = fmaf(sum[(k0 + k) % GQ], 0.0625f, v[k]);
+            }
+#pragma unroll
+            for (int g = 0; g < GQ; ++g) acc[x][g] = fmaf(sum[g], back[g], acc[x][g]);
           }
         }
-      }
-    }
-    float* slot = a.part + static_cast<int64_t>(unit + blockIdx.x) * slot_floats(gq, hd);
+        if ((w.t == w.nt - 1 || i == n - 1) && any) {
+          // the unit's partial of this warpgroup
+          float* slot = a.part + 2 * (unit + blockIdx.x) * slot_floats(a.gq, a.hd) + wg * slot_floats(a.gq, a.hd);
 #pragma unroll
-    for (int g = 0; g < 16; ++g) {
-      if (g >= gq) break;
-      const float w = warp_sum(l[g]);
-      if (lane == 0) s_red[warp][g] = w;
-      for (int cc = 0; cc < 2; ++cc)
-        if (tid + 128 * cc < hd) slot[g * hd + tid + 128 * cc] = acc[cc][g];
-    }
-    __syncthreads();
-    if (tid == 0) {
+          for (int g = 0; g < GQ; ++g) {
+            const float sum = warp_sum(l[g]);
+            if (lane == 0) s_sum[wg][quarter][g] = sum;
 #pragma unroll
-      for (int g = 0; g < 16; ++g) {
-        if (g >= gq) break;
-        slot[gq * hd + g] = m[g];
-        slot[gq * hd + gq + g] = s_red[0][g] + s_red[1][g] + s_red[2][g] + s_red[3][g];
-      }
-    }
-    x += n_run;
-    if (t == nt) {
-      t = 0;
-      if (++h == a.Hkv) {
-        h = 0;
-        do ++b;
-        while (b < a.B && (nt = tiles_of(a, b)) == 0);
-        if (b >= a.B) break;
+            for (int x = 0; x < HDA; ++x)
+              if (g < a.gq && row + 128 * x < a.hd) slot[g * a.hd + row + 128 * x] = acc[x][g];
+          }
+          named_bar_sync(1 + wg, 128);
+#pragma unroll
+          for (int g = 0; g < GQ; ++g)
+            if (row == g && g < a.gq) {
+              slot[a.gq * a.hd + g] = m[g];
+              slot[a.gq * a.hd + a.gq + g] = s_sum[wg][0][g] + s_sum[wg][1][g] + s_sum[wg][2][g] + s_sum[wg][3][g];
+            }
+          named_bar_sync(1 + wg, 128);
+        }
+        if (i + 1 < n) w.step(a);
       }
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) tmem_dealloc(tmem, Sh::tmem);
 }
 
 // Joins a unit's partials: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
@@ -424,16 +724,26 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttendArgs a) {
       for (int i = tid; i < gq * hd; i += 256) out[i] = 0.f;
     return;
   }
-  const int x0 = s_before + h * nt;
-  const int c0 = cta_of(s_total, a.ctas, x0), c1 = cta_of(s_total, a.ctas, x0 + nt - 1);
+  // the slots of the unit: each CTA whose share meets it left one for each
+  // warpgroup that had a tile of it
+  const int x0 = s_before + h * nt, x1 = x0 + nt;
+  const int c0 = cta_of(s_total, a.ctas, x0), c1 = cta_of(s_total, a.ctas, x1 - 1);
   const int sf = slot_floats(gq, hd);
-  const float* base = a.part + static_cast<int64_t>(unit) * sf;
+  const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
+  auto written = [&](int k) {
+    const Share sh = share_of(s_total, a.ctas, c0 + k / 2);
+    const int lo = max(sh.lo, x0), hi = min(sh.hi, x1);
+    return hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1);
+  };
+  const int slots = 2 * (c1 - c0 + 1);
   if (tid < gq) {
     float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, base[static_cast<int64_t>(c) * sf + gq * hd + tid]);
+    for (int k = 0; k < slots; ++k)
+      if (written(k)) M = fmaxf(M, base[static_cast<int64_t>(k) * sf + gq * hd + tid]);
     float L = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = base + static_cast<int64_t>(c) * sf + gq * hd + tid;
+    for (int k = 0; k < slots; ++k) {
+      if (!written(k)) continue;
+      const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + tid;
       L += s[gq] * (s[0] == M ? 1.f : exp2f(s[0] - M));
     }
     s_m[tid] = M;
@@ -444,8 +754,9 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttendArgs a) {
     for (int i = tid; i < gq * hd; i += 256) {
       const int g = i / hd;
       float o = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float* s = base + static_cast<int64_t>(c) * sf;
+      for (int k = 0; k < slots; ++k) {
+        if (!written(k)) continue;
+        const float* s = base + static_cast<int64_t>(k) * sf;
         const float m = s[gq * hd + g];
         o += s[i] * (m == s_m[g] ? 1.f : exp2f(m - s_m[g]));
       }
@@ -725,13 +1036,34 @@ KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
   const int gq = n_q_heads / p->n_kv_heads, hd = p->head_dim;
   const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads;
   r.tiles_cap = (p->capacity + kTile - 1) / kTile;
-  r.ctas = 8 * num_sms();
+  r.ctas = num_sms();
   const int spt = kTile / sub_rows(p->block);
-  const size_t slots = static_cast<size_t>(units + r.ctas);
+  const size_t slots = 2 * static_cast<size_t>(units + r.ctas);
   r.off_wpart = align_up(slots * slot_floats(gq, hd) * 4);
   r.off_wref = r.off_wpart + align_up(static_cast<size_t>(units) * r.tiles_cap * spt * gq * 4);
   r.bytes = r.off_wref + align_up(static_cast<size_t>(units) * r.tiles_cap * gq * 4);
   return r;
+}
+
+template <typename T, int GQ, int HDA>
+static xkv_status attend_tc_shape(const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st) {
+  constexpr int smem = AttendShape<T, GQ, HDA>::smem();
+  if (cudaFuncSetAttribute(kv8_attend_tc_kernel<T, GQ, HDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return XKV_ERR_CUDA;
+  kv8_attend_tc_kernel<T, GQ, HDA><<<a.ctas, kAttendThreads, smem, st>>>(maps[0], maps[1], a);
+  return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+}
+
+template <typename T>
+static xkv_status attend_tc(const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st) {
+  if (a.hd <= 128)
+    return a.gq <= 4   ? attend_tc_shape<T, 4, 1>(a, maps, st)
+           : a.gq <= 8 ? attend_tc_shape<T, 8, 1>(a, maps, st)
+                       : attend_tc_shape<T, 16, 1>(a, maps, st);
+  return a.gq <= 4   ? attend_tc_shape<T, 4, 2>(a, maps, st)
+         : a.gq <= 8 ? attend_tc_shape<T, 8, 2>(a, maps, st)
+                     : attend_tc_shape<T, 16, 2>(a, maps, st);
 }
 
 xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens, int n_q_heads,
@@ -761,11 +1093,18 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   a.tiles_cap = static_cast<int>(plan.tiles_cap);
   a.ctas = plan.ctas;
   a.status = device_status_ptr();
-  const size_t smem = static_cast<size_t>(a.gq) * (a.hd + kTile) * 4;
-  if (dt == XKV_BF16)
-    kv8_attend_kernel<__nv_bfloat16><<<plan.ctas, 128, smem, st>>>(a);
-  else
-    kv8_attend_kernel<float><<<plan.ctas, 128, smem, st>>>(a);
+  CUtensorMap maps[2];
+  for (int x = 0; x < 2; ++x) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(p->head_dim), static_cast<uint64_t>(p->capacity),
+                              static_cast<uint64_t>(p->batch) * p->n_kv_heads};
+    const uint64_t str[2] = {static_cast<uint64_t>(p->head_dim), static_cast<uint64_t>(p->head_dim) * p->capacity};
+    const uint32_t box[3] = {128, kTile, 1};
+    if (!make_tmap(&maps[x], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, x ? c->v : c->k, dims, str, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return XKV_ERR_CUDA;
+  }
+  const xkv_status s = dt == XKV_BF16 ? attend_tc<__nv_bfloat16>(a, maps, st) : attend_tc<float>(a, maps, st);
+  if (s != XKV_OK) return s;
   int wy = 0;
   if (accumulate) {
     const int64_t nblk = p->capacity / p->block;
