@@ -302,12 +302,17 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) {
   return r * 128u + ((((c >> 4) ^ r) & 7u) << 4) + (c & 15u);
 }
 
-// A number as a sum of e4m3 pieces: x = sum_i 16^-i piece_i.  Each piece holds
-// four significant bits and leaves a remainder of at most 2^-4 of its own, exact
-// in f32, so two pieces hold a bf16 number, six an f32 one, and five a
-// probability to 2^-20 of itself.  Numbers below 2^-6 of the first piece's scale
-// run out of exponents instead: they are held to 2^-10 16^-(pieces - 1).
-constexpr int kPiecesP = 5;
+// The small operands as several e4m3 ones.
+// Queries: x = sum_i 16^-i piece_i.  A piece holds four significant bits and
+// leaves a remainder of at most 2^-4 of itself, exact in f32: two pieces hold a
+// bf16 number and six an f32 one, down to 2^-14 of the head's largest entry for
+// two pieces (2^-30 for six), below which the last piece's exponents end.
+// Probabilities (times the value scale): fixed point against the tile's largest,
+// 28 bits in seven digits of four (24 in six for the widest tile, whose O would
+// not fit TMEM otherwise).  The codes 0 .. 15 of e4m3 stand for 0 .. 15 times
+// 2^-9 (its subnormals and first binade), so a digit is its own code.
+template <int GQ, int HDA>
+__host__ __device__ constexpr int digits() { return GQ * HDA == 32 ? 6 : 7; }
 template <typename T>
 struct Pieces;
 template <>
@@ -319,34 +324,90 @@ struct Pieces<float> {
   static constexpr int n = 6;
 };
 
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpQ = 10, kAttendThreads = 384;  // warps 0-7: softmax, two warpgroups
+// warps 0-7: softmax, two warpgroups taking tiles in turn
+constexpr int kWarpTma = 8, kWarpS = 9, kWarpO = 10, kWarpQ = 11, kAttendThreads = 384;
 constexpr int kMaxStages = 8;
 constexpr int kAtom = kTile * 128;  // bytes of 128 rows x 128 columns
 
 template <typename T, int GQ, int HDA>
 struct AttendShape {
-  static constexpr int nq = Pieces<T>::n * GQ, np = kPiecesP * GQ;          // operand rows in use
+  static constexpr int nq = Pieces<T>::n * GQ, np = digits<GQ, HDA>() * GQ;  // operand rows in use
   static constexpr int ns = (nq + 15) / 16 * 16, no = (np + 15) / 16 * 16;  // and MMA widths
-  static constexpr int tmem_used = 2 * ns + 2 * HDA * no;
-  static constexpr int tmem = tmem_used <= 64 ? 64 : tmem_used <= 128 ? 128 : tmem_used <= 256 ? 256 : 512;
-  static constexpr int bytes_p = 2 * no * 128, bytes_q = 2 * HDA * ns * 128;
-  static_assert(tmem_used <= 512, "TMEM columns");
-  static constexpr int stages() {
-    const int s = (227 * 1024 - 4096 - 1024 - bytes_p - bytes_q) / (2 * HDA * kAtom);
+  static constexpr int bytes_p = 2 * no * 128;
+  static constexpr int cols(int ahead) { return ahead * ns + 2 * HDA * no; }
+  static constexpr int stages_of(int ahead) {
+    const int s = (227 * 1024 - 8192 - 1024 - bytes_p - ahead * HDA * ns * 128) / (2 * HDA * kAtom);
     return s < kMaxStages ? s : kMaxStages;
   }
-  static constexpr int smem() { return stages() * 2 * HDA * kAtom + bytes_p + bytes_q + 1024; }
+  // S runs up to `ahead` tiles before O, in as many buffers of TMEM and of the
+  // queries' pieces.
+  static constexpr int ahead = cols(4) <= 512 && stages_of(4) >= 3   ? 4
+                               : cols(3) <= 512 && stages_of(3) >= 2 ? 3
+                               : cols(2) <= 512                      ? 2
+                                                                     : 1;
+  static constexpr int stages = stages_of(ahead);
+  static constexpr int tmem = cols(ahead) <= 64 ? 64 : cols(ahead) <= 128 ? 128 : cols(ahead) <= 256 ? 256 : 512;
+  static constexpr int bytes_q = ahead * HDA * ns * 128;
+  static_assert(cols(ahead) <= 512 && stages >= 2, "attention pipeline");
+  static constexpr int smem = stages * 2 * HDA * kAtom + bytes_p + bytes_q + 1024;
 };
+
+// Exact 2^x of a whole x <= 127; 0 below 2^-126.
+__device__ __forceinline__ float pow2_whole(float x) {
+  const int b = __float_as_int(fmaxf(x, -127.f) + 12582912.f);  // 1.5 * 2^23: x in the low bits
+  return __int_as_float((b << 23) + 0x3F800000);
+}
+
+// Sums each of p[0..GQ) over groups of `sub` (8, 16 or 32) lanes, halving the
+// values a lane holds at each of the first steps; f(g, sum) is called by one
+// lane of the group for each g.
+template <int GQ, typename F>
+__device__ __forceinline__ void group_sums(const float* p, int sub, F f) {
+  const int lane = threadIdx.x & 31;
+  float v[GQ];
+#pragma unroll
+  for (int g = 0; g < GQ; ++g) v[g] = p[g];
+  int first = 0;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const int o = 1 << s, n = GQ >> (s + 1);  // values kept by a lane after the step
+    const bool up = lane & o;
+    if (n >= 1) {
+#pragma unroll
+      for (int g = 0; g < n; ++g) {
+        const float send = up ? v[g] : v[g + n], keep = up ? v[g + n] : v[g];
+        v[g] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+      first += up ? n : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  constexpr int kLeft = GQ >= 8 ? GQ / 8 : 1;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1)
+    if (o < sub) {
+#pragma unroll
+      for (int g = 0; g < kLeft; ++g) v[g] += __shfl_xor_sync(0xffffffffu, v[g], o);
+    }
+  const int who = lane & (sub - 1);
+  if (GQ >= 8 ? who < 8 : who < 4) {
+#pragma unroll
+    for (int g = 0; g < kLeft; ++g) f(first + g, v[g]);
+  }
+}
 
 // Decode attention on the tensor cores.  For a tile of 128 token rows
 //   S = K Q^T   (128 rows x pieces of the group's queries, K = head_dim),
-//   O = V^T P^T (128 columns x pieces of the probabilities, K = 128 rows):
+//   O = V^T P^T (128 columns x digits of the probabilities, K = 128 rows):
 // the codes go from HBM to the MMA as they are (TMA, 128-byte swizzle), nothing
 // is unpacked, and the small operands carry their precision in e4m3 pieces
 // instead.  A block's scale enters as a factor of S's row or of P's column.
 //   warps 0-3, 4-7: softmax of tiles in turn; thread = token row of S, then
 //                   column of O, which is summed in f32 registers;
-//   warp 8: TMA of K and V rings; warp 9: MMA; warps 10-11: queries' pieces.
+//   warp 8: TMA of the K and V rings; warps 9, 10: the MMAs of S and of O, of
+//   their own so that neither waits for the other's operands; warp 11: the
+//   queries' pieces.
 // Rows behind the sequence's end are masked in S, and their V rows zeroed before
 // the MMA (0 * NaN).
 template <typename T, int GQ, int HDA>
@@ -354,14 +415,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const AttendArgs a) {
   using Sh = AttendShape<T, GQ, HDA>;
-  constexpr int kStages = Sh::stages(), kNq = Pieces<T>::n;
+  constexpr int kStages = Sh::stages, kAhead = Sh::ahead, kNq = Pieces<T>::n;
+  constexpr int kDigits = digits<GQ, HDA>();
+  constexpr float kDigitOne = static_cast<float>(1u << (4 * kDigits));
+  constexpr uint32_t kColO = kAhead * Sh::ns;  // O's first TMEM column, after the buffers of S
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2], done;
+  __shared__ __align__(8) uint64_t s_full[kAhead], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_total, s_before, s_b;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
-  __shared__ float s_sum[2][4][GQ], s_qc[2][GQ];
+  __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
+  __shared__ float s_sum[2][4][GQ], s_qc[kAhead][GQ];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sm;
   uint8_t* sv = sk + kStages * HDA * kAtom;
@@ -375,18 +440,22 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&q_full[i], 64);
+      mbar_init(&s_empty[i], 4);
+      mbar_init(&q_full[i], 32);
       mbar_init(&q_empty[i], 1 + 256);
     }
-    mbar_init(&done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) tmem_alloc(&s_tmem, Sh::tmem);
+  if (warp == kWarpS) tmem_alloc(&s_tmem, Sh::tmem);
   if (warp == kWarpTma && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -412,6 +481,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   // warps stop, the others run through their loops and meet every barrier.
   volatile int* abort = &s_abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (mbar_wait(bar, parity, a.status)) return true;
     *abort = 1;
@@ -446,59 +516,83 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           drain_ring(v_full, kStages, i, a.status);
         }
       }
-    } else if (warp == kWarpMma) {
-      if (lane == 0) {
-        constexpr uint32_t id_s = umma_idesc_e4m3(128, Sh::ns), id_o = umma_idesc_e4m3(128, Sh::no, true, false);
-        const int ksteps = (a.hd + 31) / 32;
-        int seg = 0;  // the unit whose S comes next
-        auto issue_s = [&](int i) {
-          const int st = i % kStages, wg = i & 1, qb = seg & 1;
-          if (i == 0 || w.t == 0) {
-            if (!wait(&q_full[qb], (seg >> 1) & 1)) return false;
-          }
-          if (!wait(&k_full[st], (i / kStages) & 1)) return false;
-          tc_fence_after();
-          for (int s = 0; s < ksteps; ++s) {
-            const int x = s / 4, o = (s % 4) * 32;
-            umma_e4m3(tmem + wg * Sh::ns, umma_desc_sw128(smem_u32(sk + (st * HDA + x) * kAtom) + o),
-                      umma_desc_sw128(smem_u32(sq + (qb * HDA + x) * Sh::ns * 128) + o), id_s, s > 0);
-          }
-          umma_commit(&s_full[wg]);
+    } else if (warp == kWarpS) {
+      // S of tile i, once its K is there and tile i - kAhead has been read out of its buffer
+      constexpr uint32_t id_s = umma_idesc_e4m3(128, Sh::ns);
+      const uint64_t dk = umma_desc_sw128(smem_u32(sk)), dq = umma_desc_sw128(smem_u32(sq));
+      const int ksteps = (a.hd + 31) / 32;
+      int st = 0, sb = 0, qb = 0;
+      uint32_t kph = 0, qph = 0, sph = 1;
+      for (int i = 0; i < n; ++i) {
+        if (i >= kAhead && !wait(&s_empty[sb], sph)) break;
+        if ((i == 0 || w.t == 0) && !wait(&q_full[qb], qph)) break;
+        if (!wait(&k_full[st], kph)) break;
+        const bool ends = w.t == w.nt - 1 || i == n - 1;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ka = dk + st * (HDA * kAtom >> 4), qa = dq + qb * (HDA * Sh::ns * 128 >> 4);
+#pragma unroll
+          for (int k = 0; k < 4 * HDA; ++k)
+            if (k < ksteps)
+              umma_e4m3(tmem + sb * Sh::ns, ka + (k / 4) * (kAtom >> 4) + (k % 4) * 2,
+                        qa + (k / 4) * (Sh::ns * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
+          umma_commit(&s_full[sb]);
           umma_commit(&k_empty[st]);
-          if (w.t == w.nt - 1 || i == n - 1) {
-            umma_commit(&q_empty[qb]);
-            ++seg;
-          }
-          if (i + 1 < n) w.step(a);
-          return true;
-        };
-        bool ok = issue_s(0);
-        if (ok && n > 1) ok = issue_s(1);
-        for (int i = 0; ok && i < n; ++i) {
-          const int st = i % kStages, wg = i & 1;
-          ok = wait(&v_full[st], (i / kStages) & 1) && wait(&p_full[wg], (i >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
+          if (ends) umma_commit(&q_empty[qb]);
+        }
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          kph ^= 1;
+        }
+        if (++sb == kAhead) {
+          sb = 0;
+          sph ^= 1;
+        }
+        if (ends && ++qb == kAhead) {
+          qb = 0;
+          qph ^= 1;
+        }
+        if (i + 1 < n) w.step(a);
+      }
+      if (elect_one()) umma_commit(&done[0]);  // what was issued ends before the CTA's memory goes
+      (void)mbar_wait(&done[0], 0, a.status);
+    } else if (warp == kWarpO) {
+      constexpr uint32_t id_o = umma_idesc_e4m3(128, Sh::no, true, false);
+      const uint64_t dv = umma_desc_sw128_mn(smem_u32(sv), kAtom, 1024), dp = umma_desc_sw128(smem_u32(sp));
+      int st = 0;
+      uint32_t vph = 0;
+      for (int i = 0; i < n; ++i) {
+        const int wg = i & 1;
+        if (!wait(&v_full[st], vph) || !wait(&p_full[wg], (i >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t va = dv + st * (HDA * kAtom >> 4), pa = dp + wg * (Sh::no * 128 >> 4);
+#pragma unroll
           for (int x = 0; x < HDA; ++x)
-            for (int s = 0; s < 4; ++s)
-              umma_e4m3(tmem + 2 * Sh::ns + (wg * HDA + x) * Sh::no,
-                        umma_desc_sw128_mn(smem_u32(sv + (st * HDA + x) * kAtom) + s * 4096, kAtom, 1024),
-                        umma_desc_sw128(smem_u32(sp + wg * Sh::no * 128) + s * 32), id_o, s > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_e4m3(tmem + kColO + (wg * HDA + x) * Sh::no, va + x * (kAtom >> 4) + k * (4096 >> 4), pa + k * 2,
+                        id_o, k > 0);
           umma_commit(&o_full[wg]);
           umma_commit(&v_empty[st]);
-          if (i + 2 < n) ok = issue_s(i + 2);
         }
-        umma_commit(&done);  // what was issued ends before the CTA's memory goes
-        (void)mbar_wait(&done, 0, a.status);
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          vph ^= 1;
+        }
       }
-    } else if (warp >= kWarpQ) {
+      if (elect_one()) umma_commit(&done[1]);
+      (void)mbar_wait(&done[1], 0, a.status);
+    } else if (warp == kWarpQ) {
       // queries of one unit: pieces, K-major rows piece * GQ + g, zero past head_dim and past the group
       int seg = 0;
       for (int i = 0; i < n;) {
-        const int qb = seg & 1;
-        if (seg >= 2) (void)wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1);
+        const int qb = seg % kAhead;
+        if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
         const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
-        for (int g = warp - kWarpQ; g < GQ; g += 2) {
+        for (int g = 0; g < GQ; ++g) {
           const T* q = static_cast<const T*>(a.q) + (unit * a.gq + g) * a.hd;
           float x[4 * HDA];
           uint32_t big = 0;
@@ -539,39 +633,86 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     } else {
       const int wg = warp >> 2, row = tid & 127, quarter = warp & 3;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      const int64_t nblk = a.capacity / a.block;
-      const int sub = sub_rows(a.block);
+      const int lb = 31 - __clz(a.block), sub = sub_rows(a.block), ls = min(lb, 5), spt = kTile >> ls;
+      const int64_t nblk = a.capacity >> lb;
       uint8_t* p_op = sp + wg * Sh::no * 128;
-      float acc[HDA][GQ], m[GQ], l[GQ], c[GQ];
-      bool any = false;
-      int seg = 0;
-      for (int i = 0; i < n; ++i) {
-        const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
-        if (i == 0 || w.t == 0) {
-          const int qb = seg & 1;
-          (void)wait(&q_full[qb], (seg >> 1) & 1);
+      float acc[HDA][GQ], l[GQ], c[GQ];
+      float m = -INFINITY;  // lane g: the running reference of head g, a whole number
+      // O of use `u` (the u-th tile of this warpgroup) into the sums
+      auto fold = [&](int u) {
+        (void)wait(&o_full[wg], u & 1);
+        tc_fence_after();
+        const float4* ref = s_ref[wg][u & 1][quarter];
+#pragma unroll
+        for (int x = 0; x < HDA; ++x) {
+          float sum[GQ];
+#pragma unroll
+          for (int g = 0; g < GQ; ++g) sum[g] = 0.f;
+          // the pieces' columns from the least on, at most 48 registers of them at a time
+          constexpr int kCols = Sh::no <= 48 ? Sh::no : 32;
+#pragma unroll
+          for (int k0 = (Sh::no - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
+            float v[kCols];
+#pragma unroll
+            for (int k = 0; k < kCols; k += 16)
+              if (k0 + k < Sh::no) tmem_ld16(tmem + lanes + kColO + (wg * HDA + x) * Sh::no + k0 + k, v + k);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = kCols - 1; k >= 0; --k)
+              if (k0 + k < Sh::np) sum[(k0 + k) % GQ] = fmaf(sum[(k0 + k) % GQ], 0.0625f, v[k]);
+          }
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
-            c[g] = s_qc[qb][g];
-            m[g] = -INFINITY;
-            l[g] = 0.f;
-#pragma unroll
-            for (int x = 0; x < HDA; ++x) acc[x][g] = 0.f;
+            const float2 r = *reinterpret_cast<const float2*>(&ref[g].z);
+            acc[x][g] = fmaf(sum[g], r.y, acc[x][g] * r.x);
           }
-          mbar_arrive(&q_empty[qb]);
-          any = false;
-          ++seg;
         }
-        if ((i & 1) == wg) {
-          any = true;
-          const int use = i >> 1, par = use & 1;
-          const int64_t at = static_cast<int64_t>(w.t) * kTile + row;
-          const bool live = at < w.len;
-          const float ks = live ? __ldg(a.k_scale + unit * nblk + at / a.block) : 0.f;
-          const float vs = live ? __ldg(a.v_scale + unit * nblk + at / a.block) : 0.f;
-          float s[GQ];
-          (void)wait(&s_full[wg], par);
+      };
+      int seg = 0;
+      for (int i0 = 0; i0 < n; ++seg) {
+        // one unit: tiles i0 .. i1 - 1 of the share, t0 ... of the unit; this warpgroup's are every other one
+        const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+        const int t0 = w.t, i1 = min(n, i0 + w.nt - t0);
+        const int first = i0 + ((i0 ^ wg) & 1);
+        const int len = static_cast<int>(w.len);
+        const float* ksp = a.k_scale + unit * nblk;
+        const float* vsp = a.v_scale + unit * nblk;
+        float* wp = a.wpart ? a.wpart + unit * a.tiles_cap * spt * a.gq : nullptr;
+        float* wr = a.wref + unit * a.tiles_cap * a.gq;
+        int at = (t0 + first - i0) * kTile + row;
+        // scales of the warpgroup's tiles, loaded two of them ahead
+        float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f;
+        auto scales = [&](int k, float* x, float* y) {
+          const int r = at + k * 2 * kTile;
+          if (first + 2 * k < i1 && r < len) {
+            *x = __ldg(ksp + (r >> lb));
+            *y = __ldg(vsp + (r >> lb));
+          }
+        };
+        scales(0, &ks, &vs);
+        scales(1, &ks1, &vs1);
+        const int qb = seg % kAhead;
+        (void)wait(&q_full[qb], (seg / kAhead) & 1);
+#pragma unroll
+        for (int g = 0; g < GQ; ++g) {
+          c[g] = s_qc[qb][g];
+          l[g] = 0.f;
+#pragma unroll
+          for (int x = 0; x < HDA; ++x) acc[x][g] = 0.f;
+        }
+        m = -INFINITY;
+        mbar_arrive(&q_empty[qb]);
+        for (int i = first; i < i1; i += 2, at += 2 * kTile) {
+          const int use = i >> 1, par = use & 1, sb = i % kAhead, t = t0 + i - i0;
+          const bool live = at < len;
+          (void)wait(&s_full[sb], (i / kAhead) & 1);
           tc_fence_after();
+          float ks2 = 0.f, vs2 = 0.f;
+          if (i + 4 < i1 && at + 4 * kTile < len) {
+            ks2 = __ldg(ksp + ((at + 4 * kTile) >> lb));
+            vs2 = __ldg(vsp + ((at + 4 * kTile) >> lb));
+          }
+          float s[GQ];
 #pragma unroll
           for (int g = 0; g < GQ; ++g) s[g] = 0.f;
           constexpr int kCols = Sh::ns <= 48 ? Sh::ns : 48;
@@ -579,62 +720,57 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           for (int k0 = (Sh::ns - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
             float v[kCols];
 #pragma unroll
-            for (int k = 0; k < kCols; k += 16) tmem_ld16(tmem + lanes + wg * Sh::ns + k0 + k, v + k);
+            for (int k = 0; k < kCols; k += 16) tmem_ld16(tmem + lanes + sb * Sh::ns + k0 + k, v + k);
             tmem_ld_wait();
 #pragma unroll
             for (int k = kCols - 1; k >= 0; --k)
               if (k0 + k < Sh::nq) s[(k0 + k) % GQ] = fmaf(s[(k0 + k) % GQ], 0.0625f, v[k]);
           }
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&s_empty[sb]);
           // The tile's largest logits, and the largest of logit + log2(value scale), which is what a row brings to
-          // O: both as whole numbers, so that every change of reference is an exact power of two.
-          const float ev = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
-          const float vm = live ? __uint_as_float((__float_as_uint(vs) & 0x7FFFFFu) | 0x3F800000u) * 128.f : 0.f;
+          // O: references are whole numbers, so that every change of one is an exact power of two.
+          const uint32_t vb = __float_as_uint(vs), frac = vb & 0x7FFFFFu;  // vs = vm 2^ev, vm in (1/2, 1]
+          const float ev = static_cast<float>(static_cast<int>(vb >> 23) - 127 + (frac ? 1 : 0));
+          const float vm = live ? __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kDigitOne : 0.f;
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
-            const float t = live ? s[g] * (c[g] * ks) : -INFINITY;
-            const float t0 = redux_max(t), t1 = redux_max(t + ev);
+            const float x = live ? s[g] * (c[g] * ks) : -INFINITY;
+            const float x0 = redux_max(x), x1 = redux_max(x + ev);
             if (lane == 0) {
-              s_max[wg][par][2 * g][quarter] = t0;
-              s_max[wg][par][2 * g + 1][quarter] = t1;
+              s_max[wg][par][2 * g][quarter] = x0;
+              s_max[wg][par][2 * g + 1][quarter] = x1;
             }
           }
           named_bar_sync(1 + wg, 128);
-          float* wp = a.wpart ? a.wpart + (unit * a.tiles_cap + w.t) * (kTile / sub) * a.gq : nullptr;
-          float back[GQ];
+          float4* ref = s_ref[wg][par][quarter];  // {reference, -reference of O, factors of the sums and of O}
+          if (lane < GQ) {
+            const float4 x0 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * lane]);
+            const float4 x1 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * lane + 1]);
+            const float mn = fmaxf(m, ceilf(fmaxf(fmaxf(x0.x, x0.y), fmaxf(x0.z, x0.w))));
+            const float mv = ceilf(fmaxf(fmaxf(x1.x, x1.y), fmaxf(x1.z, x1.w)));
+            const float al = m == mn ? 1.f : pow2_whole(m - mn);
+            // O's digits are 2^-9 of what they stand for, its sum is in units of the highest, 1 is 16 of those
+            ref[lane] = make_float4(mn, mv, al, ex2(mv - mn) * (512.f / 16.f));
+            m = mn;
+          }
+          if (use > 0 && i > first) fold(use - 1);
+          __syncwarp();
+          float p[GQ];
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
-            const float4 t0 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * g]);
-            const float4 t1 = *reinterpret_cast<const float4*>(s_max[wg][par][2 * g + 1]);
-            const float mn = fmaxf(m[g], ceilf(fmaxf(fmaxf(t0.x, t0.y), fmaxf(t0.z, t0.w))));
-            const float mv = ceilf(fmaxf(fmaxf(t1.x, t1.y), fmaxf(t1.z, t1.w)));
-            const float al = m[g] == mn ? 1.f : ex2(m[g] - mn);
-            m[g] = mn;
-            back[g] = ex2(mv - mn) * (1.f / 128.f);
-            const float p = live ? ex2(fmaf(s[g], c[g] * ks, -mn)) : 0.f;
-            l[g] = fmaf(l[g], al, p);
+            const float4 r = ref[g];
+            const float ck = c[g] * ks;
+            p[g] = live ? ex2(fmaf(s[g], ck, -r.x)) : 0.f;
+            l[g] = fmaf(l[g], r.z, p[g]);
+            // a NaN is 0 here; the sum l has it
+            const uint32_t fix = min(__float2uint_rn(live ? ex2(fmaf(s[g], ck, ev - r.y)) * vm : 0.f),
+                                     (1u << (4 * kDigits)) - 1u);
 #pragma unroll
-            for (int x = 0; x < HDA; ++x) acc[x][g] *= al;
-            s[g] = live ? ex2(fmaf(s[g], c[g] * ks, ev - mv)) * vm : 0.f;
-            if (wp && g < a.gq) {
-              float sum = p;
-              for (int o = 1; o < sub; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              if (row % sub == 0) wp[(row / sub) * a.gq + g] = sum;
-              if (row == 0) a.wref[(unit * a.tiles_cap + w.t) * a.gq + g] = mn;
-            }
+            for (int k = 0; k < kDigits; ++k)
+              p_op[swz128(k * GQ + g, row)] = static_cast<uint8_t>((fix >> (4 * (kDigits - 1 - k))) & 15u);
           }
-#pragma unroll
-          for (int p = 0; p < kPiecesP; ++p) {
-#pragma unroll
-            for (int g = 0; g < GQ; g += 2) {
-              const uint16_t e = to_e4m3x2(s[g], s[g + 1]);
-              const float2 f = from_e4m3x2(e);
-              s[g] = 16.f * (s[g] - f.x);
-              s[g + 1] = 16.f * (s[g + 1] - f.y);
-              p_op[swz128(p * GQ + g, row)] = static_cast<uint8_t>(e);
-              p_op[swz128(p * GQ + g + 1, row)] = static_cast<uint8_t>(e >> 8);
-            }
-          }
-          if (w.len - static_cast<int64_t>(w.t) * kTile < kTile) {
+          if (len - t * kTile < kTile) {
             const int st = i % kStages;
             (void)wait(&v_full[st], (i / kStages) & 1);
             if (!live) {
@@ -648,34 +784,22 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           fence_proxy_async();
           tc_fence_before();
           mbar_arrive(&p_full[wg]);
-          (void)wait(&o_full[wg], par);
-          tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < HDA; ++x) {
-            float sum[GQ];
-#pragma unroll
-            for (int g = 0; g < GQ; ++g) sum[g] = 0.f;
-            // the pieces' columns from the least on, at most 48 registers of them at a time
-            constexpr int kCols = Sh::no <= 48 ? Sh::no : 32;
-#pragma unroll
-            for (int k0 = (Sh::no - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
-              float v[kCols];
-#pragma unroll
-              for (int k = 0; k < kCols; k += 16)
-                if (k0 + k < Sh::no)
-                  tmem_ld16(tmem + lanes + 2 * Sh::ns + (wg * HDA + x) * Sh::no + k0 + k, v + k);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = kCols - 1; k >= 0; --k)
-                if (k0 + k < Sh::np) sum[(k0 + k) % GQ] = fmaf(sum[(k0 + k) % GQ], 0.0625f, v[k]);
-            }
-#pragma unroll
-            for (int g = 0; g < GQ; ++g) acc[x][g] = fmaf(sum[g], back[g], acc[x][g]);
+          if (wp) {
+            float* wt = wp + (static_cast<int64_t>(t) * spt + (row >> ls)) * a.gq;
+            group_sums<GQ>(p, sub, [&](int g, float sum) {
+              if (g < a.gq) wt[g] = sum;
+            });
+            if (quarter == 0 && lane < a.gq) wr[static_cast<int64_t>(t) * a.gq + lane] = m;
           }
+          ks = ks1;
+          vs = vs1;
+          ks1 = ks2;
+          vs1 = vs2;
         }
-        if ((w.t == w.nt - 1 || i == n - 1) && any) {
+        if (first < i1) {
           // the unit's partial of this warpgroup
-          float* slot = a.part + 2 * (unit + blockIdx.x) * slot_floats(a.gq, a.hd) + wg * slot_floats(a.gq, a.hd);
+          fold(((i1 - 1 - wg) & ~1) / 2);
+          float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * slot_floats(a.gq, a.hd);
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
             const float sum = warp_sum(l[g]);
@@ -685,33 +809,41 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
               if (g < a.gq && row + 128 * x < a.hd) slot[g * a.hd + row + 128 * x] = acc[x][g];
           }
           named_bar_sync(1 + wg, 128);
-#pragma unroll
-          for (int g = 0; g < GQ; ++g)
-            if (row == g && g < a.gq) {
-              slot[a.gq * a.hd + g] = m[g];
-              slot[a.gq * a.hd + a.gq + g] = s_sum[wg][0][g] + s_sum[wg][1][g] + s_sum[wg][2][g] + s_sum[wg][3][g];
-            }
+          if (row < a.gq) {
+            slot[a.gq * a.hd + row] = m;
+            slot[a.gq * a.hd + a.gq + row] = s_sum[wg][0][row] + s_sum[wg][1][row] + s_sum[wg][2][row] + s_sum[wg][3][row];
+          }
           named_bar_sync(1 + wg, 128);
         }
-        if (i + 1 < n) w.step(a);
+        // to the next unit
+        i0 = i1;
+        if (i0 < n) {
+          w.t = w.nt - 1;
+          w.step(a);
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) tmem_dealloc(tmem, Sh::tmem);
+  if (warp == kWarpS) tmem_dealloc(tmem, Sh::tmem);
 }
 
 // Joins a unit's partials: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
-// CTA (unit, 0) writes the output; CTAs (unit, y > 0) add a share of the blocks'
-// weights, sum_g 2^(ref - M_g) wpart / L_g.
-__global__ void __launch_bounds__(256) kv8_combine_kernel(const AttendArgs a) {
+// CTA (unit, y < gq) writes head y's output, warp by slot; CTAs (unit, y >= gq)
+// add a share of the blocks' weights, sum_g 2^(ref - M_g) wpart / L_g.
+constexpr int kCombineThreads = 256;
+constexpr int kMaxSlots = 2 * 256;  // of one unit: two for each CTA
+
+__global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttendArgs a) {
   __shared__ int s_before, s_total;
-  __shared__ float s_m[16], s_l[16];
-  const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x, gq = a.gq, hd = a.hd;
-  if (tid < 32) {
+  __shared__ float s_f[kMaxSlots];
+  __shared__ float s_m[16], s_r[16], s_red[8][256];
+  const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (warp == 0) {
     const Line l = walk_line(a, b, -1);
-    if (tid == 0) {
+    if (lane == 0) {
       s_before = l.before;
       s_total = l.total;
     }
@@ -720,62 +852,94 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttendArgs a) {
   const int nt = tiles_of(a, b);
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
-    if (blockIdx.y == 0)
-      for (int i = tid; i < gq * hd; i += 256) out[i] = 0.f;
+    if (static_cast<int>(blockIdx.y) < gq)
+      for (int i = tid; i < hd; i += kCombineThreads) out[blockIdx.y * hd + i] = 0.f;
     return;
   }
   // the slots of the unit: each CTA whose share meets it left one for each
   // warpgroup that had a tile of it
   const int x0 = s_before + h * nt, x1 = x0 + nt;
   const int c0 = cta_of(s_total, a.ctas, x0), c1 = cta_of(s_total, a.ctas, x1 - 1);
-  const int sf = slot_floats(gq, hd);
+  const int sf = slot_floats(gq, hd), slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
   auto written = [&](int k) {
     const Share sh = share_of(s_total, a.ctas, c0 + k / 2);
     const int lo = max(sh.lo, x0), hi = min(sh.hi, x1);
     return hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1);
   };
-  const int slots = 2 * (c1 - c0 + 1);
-  if (tid < gq) {
+  // by one warp: head g's largest reference and sum, and (factors) every slot's 2^(m - M) into s_f
+  auto head = [&](int g, bool factors) {
     float M = -INFINITY;
-    for (int k = 0; k < slots; ++k)
-      if (written(k)) M = fmaxf(M, base[static_cast<int64_t>(k) * sf + gq * hd + tid]);
+    for (int k = lane; k < slots; k += 32)
+      if (written(k)) M = fmaxf(M, base[static_cast<int64_t>(k) * sf + gq * hd + g]);
+    M = warp_max(M);
     float L = 0.f;
-    for (int k = 0; k < slots; ++k) {
-      if (!written(k)) continue;
-      const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + tid;
-      L += s[gq] * (s[0] == M ? 1.f : exp2f(s[0] - M));
-    }
-    s_m[tid] = M;
-    s_l[tid] = L;
-  }
-  __syncthreads();
-  if (blockIdx.y == 0) {
-    for (int i = tid; i < gq * hd; i += 256) {
-      const int g = i / hd;
-      float o = 0.f;
-      for (int k = 0; k < slots; ++k) {
-        if (!written(k)) continue;
-        const float* s = base + static_cast<int64_t>(k) * sf;
-        const float m = s[gq * hd + g];
-        o += s[i] * (m == s_m[g] ? 1.f : exp2f(m - s_m[g]));
+    for (int k = lane; k < slots; k += 32) {
+      float f = 0.f;
+      if (written(k)) {
+        const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + g;
+        f = s[0] == M ? 1.f : exp2f(s[0] - M);
+        L += s[gq] * f;
       }
-      out[i] = o / s_l[g];
+      if (factors) s_f[k] = f;
+    }
+    L = warp_sum(L);
+    if (lane == 0) {
+      s_m[g] = M;
+      s_r[g] = 1.f / L;
+    }
+  };
+  if (static_cast<int>(blockIdx.y) < gq) {
+    const int g = blockIdx.y;
+    if (warp == 0) head(g, true);
+    __syncthreads();
+    float acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    const int per = hd / 16;  // columns in pairs: lane and 16-column steps
+    for (int k = warp; k < slots; k += 8) {
+      const float f = s_f[k];
+      const float2* s = reinterpret_cast<const float2*>(base + static_cast<int64_t>(k) * sf + g * hd);
+      // an unwritten slot holds anything
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = e * 32 + lane;
+        if (col < per * 8) {
+          const float2 v = f != 0.f ? s[col] : make_float2(0.f, 0.f);
+          acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int col = e * 32 + lane;
+      if (col < per * 8) *reinterpret_cast<float2*>(&s_red[warp][2 * col]) = make_float2(acc[2 * e], acc[2 * e + 1]);
+    }
+    __syncthreads();
+    if (tid < hd) {
+      float o = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o += s_red[k][tid];
+      out[g * hd + tid] = o * s_r[g];
     }
     return;
   }
+  for (int g = warp; g < gq; g += 8) head(g, false);
+  __syncthreads();
   const int64_t nblk = a.capacity / a.block;
   const int n = static_cast<int>((checked_len(a.lens[b], a.capacity, nullptr) + a.block - 1) / a.block);
   const int sub = sub_rows(a.block), spb = a.block / sub, spt = kTile / sub;
-  for (int k = (blockIdx.y - 1) * 256 + tid; k < n; k += (gridDim.y - 1) * 256) {
+  for (int k = (blockIdx.y - gq) * kCombineThreads + tid; k < n; k += (gridDim.y - gq) * kCombineThreads) {
     float w = 0.f;
     const int64_t s0 = static_cast<int64_t>(k) * spb, tile = s0 / spt;
     const float* ref = a.wref + (static_cast<int64_t>(unit) * a.tiles_cap + tile) * gq;
     const float* p = a.wpart + (static_cast<int64_t>(unit) * a.tiles_cap * spt + s0) * gq;
+#pragma unroll 4
     for (int g = 0; g < gq; ++g) {
-      float s = 0.f;
-      for (int e = 0; e < spb; ++e) s += p[e * gq + g];
-      w += s * exp2f(ref[g] - s_m[g]) / s_l[g];
+      float s = p[g];
+      for (int e = 1; e < spb; ++e) s += p[e * gq + g];
+      w = fmaf(s, exp2f(ref[g] - s_m[g]) * s_r[g], w);
     }
     a.weight[unit * nblk + k] += w;
   }
@@ -1036,7 +1200,7 @@ KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
   const int gq = n_q_heads / p->n_kv_heads, hd = p->head_dim;
   const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads;
   r.tiles_cap = (p->capacity + kTile - 1) / kTile;
-  r.ctas = num_sms();
+  r.ctas = std::min(num_sms(), kMaxSlots / 2);
   const int spt = kTile / sub_rows(p->block);
   const size_t slots = 2 * static_cast<size_t>(units + r.ctas);
   r.off_wpart = align_up(slots * slot_floats(gq, hd) * 4);
@@ -1047,7 +1211,7 @@ KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
 
 template <typename T, int GQ, int HDA>
 static xkv_status attend_tc_shape(const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st) {
-  constexpr int smem = AttendShape<T, GQ, HDA>::smem();
+  constexpr int smem = AttendShape<T, GQ, HDA>::smem;
   if (cudaFuncSetAttribute(kv8_attend_tc_kernel<T, GQ, HDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return XKV_ERR_CUDA;
@@ -1108,9 +1272,9 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   int wy = 0;
   if (accumulate) {
     const int64_t nblk = p->capacity / p->block;
-    wy = static_cast<int>(std::min<int64_t>((nblk + 255) / 256, 64));
+    wy = static_cast<int>(std::min<int64_t>((nblk + kCombineThreads - 1) / kCombineThreads, 64));
   }
-  kv8_combine_kernel<<<dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads, 1 + wy), 256, 0, st>>>(a);
+  kv8_combine_kernel<<<dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads, a.gq + wy), kCombineThreads, 0, st>>>(a);
   return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
 }
 

@@ -4,8 +4,11 @@ Codes, scales, ids and eviction are exact: every rounding they hold is of an exa
 f32 arithmetic; with S the largest |logit| of a case, a probability is off by its logit's absolute error (at most
 8 half-ulps of a number of size S: the product's accumulation, its scaling and the subtraction) and by 64 half-ulps
 for everything else (exp2, the split of the probability into pieces, the sums over tokens and partials, the
-division), so a row of the output is within 2^-24 (8 S + 64) of the row's norm, plus as much of what the values'
-cancellation leaves: the bound is taken against sum_t p_t |v_t|, which no cancellation shrinks."""
+division), so an output is within 2^-24 (8 S + 64) of sum_t p_t |v_t|, which no cancellation shrinks.  A row's
+probability times its block's value scale enters the product with the codes in fixed point, seven digits of four bits
+(six for more than 8 query heads of more than 128 columns) of a number that the largest of the 128-row tile is at
+least half of: rounding to the last digit's half, or 1 to the largest number below it, leaves at most 2^-28 (2^-24)
+and so 2^-27 (2^-23) of the tile's largest, times the rows' codes."""
 import numpy as np
 import pytest
 import torch
@@ -75,10 +78,24 @@ def _fill(xkv, B, H, hd, block, capacity, counts, dt="bf16", seed=0):
 
 
 def _bounds(b, q, top):
-    """Row by row: 2^-24 (8 S + 64) sum_t p_t |v_t|, and the same for the blocks' weights."""
+    """Output by output: 2^-24 (8 S + 64) sum_t p_t |v_t|, and the fixed point's share."""
     a = dict(b.r)
     a["v"] = np.abs(b.r["v"])
-    return 2.0 ** -24 * (8 * top + 64) * ref.attend(a, b.block, b.lens, q)[0]
+    tol = 2.0 ** -24 * (8 * top + 64) * ref.attend(a, b.block, b.lens, q)[0]
+    H = b.r["k"].shape[1]
+    gq = q.shape[1] // H
+    fixed = 2.0 ** (-23 if gq > 8 and q.shape[2] > 128 else -27)
+    for i, n in enumerate(b.lens):
+        at = np.arange(n) // b.block
+        for h in range(H if n else 0):
+            k = b.r["k"][i, h, :n] * b.r["k_scale"][i, h, at][:, None]
+            s = q[i, h * gq:(h + 1) * gq] @ k.T / np.sqrt(q.shape[2])
+            p = np.exp(s - s.max(1, keepdims=True))
+            p *= b.r["v_scale"][i, h, at] / p.sum(1, keepdims=True)
+            for t in range(0, n, 128):
+                most = p[:, t:t + 128].max(1)
+                tol[i, h * gq:(h + 1) * gq] += fixed * most[:, None] * a["v"][i, h, t:min(t + 128, n)].sum(0)
+    return tol
 
 
 def _attend(b, q, accumulate=False, ws=None, stream=None, out=None):
