@@ -308,11 +308,20 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) {
 // bf16 number and six an f32 one, down to 2^-14 of the head's largest entry for
 // two pieces (2^-30 for six), below which the last piece's exponents end.
 // Probabilities (times the value scale): fixed point against the tile's largest,
-// 28 bits in seven digits of four (24 in six for the widest tile, whose O would
+// 32 bits in eight digits of four (24 in six for the widest tile, whose O would
 // not fit TMEM otherwise).  The codes 0 .. 15 of e4m3 stand for 0 .. 15 times
 // 2^-9 (its subnormals and first binade), so a digit is its own code.
 template <int GQ, int HDA>
-__host__ __device__ constexpr int digits() { return GQ * HDA == 32 ? 6 : 7; }
+__host__ __device__ constexpr int digits() { return GQ * HDA == 32 ? 6 : 8; }
+
+// Four digits as four bytes: of byte i of a and byte j of b (with six digits,
+// a and b are below 2^24).
+template <int D>
+__device__ __forceinline__ uint32_t spread(uint32_t a, int i, uint32_t b, int j) {
+  const uint32_t y = D == 8 ? __byte_perm(a, 0u, 0x4040u | i | j << 8)  // one number's bytes i, j
+                            : __byte_perm(a, b, 0x7430u | i | j << 8);
+  return (y | y << 4) & 0x0F0F0F0Fu;
+}
 template <typename T>
 struct Pieces;
 template <>
@@ -332,7 +341,7 @@ constexpr int kAtom = kTile * 128;  // bytes of 128 rows x 128 columns
 template <typename T, int GQ, int HDA>
 struct AttendShape {
   static constexpr int nq = Pieces<T>::n * GQ, np = digits<GQ, HDA>() * GQ;  // operand rows in use
-  static constexpr int ns = (nq + 15) / 16 * 16, no = (np + 15) / 16 * 16;  // and MMA widths
+  static constexpr int ns = (nq + 15) / 16 * 16, no = np;                // and MMA widths
   static constexpr int bytes_p = 2 * no * 128;
   static constexpr int cols(int ahead) { return ahead * ns + 2 * HDA * no; }
   static constexpr int stages_of(int ahead) {
@@ -417,7 +426,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   using Sh = AttendShape<T, GQ, HDA>;
   constexpr int kStages = Sh::stages, kAhead = Sh::ahead, kNq = Pieces<T>::n;
   constexpr int kDigits = digits<GQ, HDA>();
-  constexpr float kDigitOne = static_cast<float>(1u << (4 * kDigits));
+  constexpr float kDigitOne = kDigits == 8 ? 4294967296.f : 16777216.f;
   constexpr uint32_t kColO = kAhead * Sh::ns;  // O's first TMEM column, after the buffers of S
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
@@ -558,8 +567,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       if (elect_one()) umma_commit(&done[0]);  // what was issued ends before the CTA's memory goes
       (void)mbar_wait(&done[0], 0, a.status);
     } else if (warp == kWarpO) {
-      constexpr uint32_t id_o = umma_idesc_e4m3(128, Sh::no, true, false);
-      const uint64_t dv = umma_desc_sw128_mn(smem_u32(sv), kAtom, 1024), dp = umma_desc_sw128(smem_u32(sp));
+      constexpr uint32_t id_o = umma_idesc_e4m3(128, Sh::no, true, true);
+      const uint64_t dv = umma_desc_sw128_mn(smem_u32(sv), kAtom, 1024), dp = umma_desc_sw32_mn(smem_u32(sp), kTile * 32, 256);
       int st = 0;
       uint32_t vph = 0;
       for (int i = 0; i < n; ++i) {
@@ -572,7 +581,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           for (int x = 0; x < HDA; ++x)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_e4m3(tmem + kColO + (wg * HDA + x) * Sh::no, va + x * (kAtom >> 4) + k * (4096 >> 4), pa + k * 2,
+              umma_e4m3(tmem + kColO + (wg * HDA + x) * Sh::no, va + x * (kAtom >> 4) + k * (4096 >> 4), pa + k * (1024 >> 4),
                         id_o, k > 0);
           umma_commit(&o_full[wg]);
           umma_commit(&v_empty[st]);
@@ -635,7 +644,9 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
       const int lb = 31 - __clz(a.block), sub = sub_rows(a.block), ls = min(lb, 5), spt = kTile >> ls;
       const int64_t nblk = a.capacity >> lb;
-      uint8_t* p_op = sp + wg * Sh::no * 128;
+      // this token's row of P: 32 bytes in each block of 32 digits, 16-byte halves swapped by the 32-byte swizzle
+      uint8_t* p_row = sp + wg * Sh::no * 128 + row * 32;
+      const int p_flip = (row & 4) << 2;
       float acc[HDA][GQ], l[GQ], c[GQ];
       float m = -INFINITY;  // lane g: the running reference of head g, a whole number
       // O of use `u` (the u-th tile of this warpgroup) into the sums
@@ -648,18 +659,16 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           float sum[GQ];
 #pragma unroll
           for (int g = 0; g < GQ; ++g) sum[g] = 0.f;
-          // the pieces' columns from the least on, at most 48 registers of them at a time
-          constexpr int kCols = Sh::no <= 48 ? Sh::no : 32;
+          constexpr int kHeads = kDigits == 8 ? 4 : 8, kCols = kHeads * kDigits;  // heads read at a time
 #pragma unroll
-          for (int k0 = (Sh::no - 1) / kCols * kCols; k0 >= 0; k0 -= kCols) {
+          for (int g0 = 0; g0 < GQ; g0 += kHeads) {
             float v[kCols];
 #pragma unroll
             for (int k = 0; k < kCols; k += 16)
-              if (k0 + k < Sh::no) tmem_ld16(tmem + lanes + kColO + (wg * HDA + x) * Sh::no + k0 + k, v + k);
+              tmem_ld16(tmem + lanes + kColO + (wg * HDA + x) * Sh::no + g0 * kDigits + k, v + k);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = kCols - 1; k >= 0; --k)
-              if (k0 + k < Sh::np) sum[(k0 + k) % GQ] = fmaf(sum[(k0 + k) % GQ], 0.0625f, v[k]);
+            for (int k = 0; k < kCols; ++k) sum[g0 + k / kDigits] = fmaf(sum[g0 + k / kDigits], 0.0625f, v[k]);
           }
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
@@ -757,18 +766,27 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           if (use > 0 && i > first) fold(use - 1);
           __syncwarp();
           float p[GQ];
+          uint32_t fix[GQ];
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
             const float4 r = ref[g];
             const float ck = c[g] * ks;
             p[g] = live ? ex2(fmaf(s[g], ck, -r.x)) : 0.f;
             l[g] = fmaf(l[g], r.z, p[g]);
-            // a NaN is 0 here; the sum l has it
-            const uint32_t fix = min(__float2uint_rn(live ? ex2(fmaf(s[g], ck, ev - r.y)) * vm : 0.f),
-                                     (1u << (4 * kDigits)) - 1u);
+            // a NaN is 0 here, and the sum l has it; 1 itself is the largest number below it
+            fix[g] = __float2uint_rn(live ? ex2(fmaf(s[g], ck, ev - r.y)) * vm : 0.f);
+            if (kDigits < 8) fix[g] = min(fix[g], (1u << (4 * (kDigits & 7))) - 1u);
+          }
 #pragma unroll
-            for (int k = 0; k < kDigits; ++k)
-              p_op[swz128(k * GQ + g, row)] = static_cast<uint8_t>((fix >> (4 * (kDigits - 1 - k))) & 15u);
+          for (int k = 0; k < Sh::no / 16; ++k) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int m = 8 * k + 2 * e, n1 = m + 1;  // the word's bytes in the row of numbers
+              o[e] = spread<kDigits>(fix[m / (kDigits / 2)], m % (kDigits / 2), fix[n1 / (kDigits / 2)], n1 % (kDigits / 2));
+            }
+            *reinterpret_cast<uint4*>(p_row + (k / 2) * kTile * 32 + (((k & 1) * 16) ^ p_flip)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
           }
           if (len - t * kTile < kTile) {
             const int st = i % kStages;

@@ -5,10 +5,10 @@ f32 arithmetic; with S the largest |logit| of a case, a probability is off by it
 8 half-ulps of a number of size S: the product's accumulation, its scaling and the subtraction) and by 64 half-ulps
 for everything else (exp2, the split of the probability into pieces, the sums over tokens and partials, the
 division), so an output is within 2^-24 (8 S + 64) of sum_t p_t |v_t|, which no cancellation shrinks.  A row's
-probability times its block's value scale enters the product with the codes in fixed point, seven digits of four bits
-(six for more than 8 query heads of more than 128 columns) of a number that the largest of the 128-row tile is at
-least half of: rounding to the last digit's half, or 1 to the largest number below it, leaves at most 2^-28 (2^-24)
-and so 2^-27 (2^-23) of the tile's largest, times the rows' codes."""
+probability times its block's value scale enters the product with the codes in fixed point, 28 bits at least (24 for
+more than 8 query heads of more than 128 columns) of a number that the largest of the 128-row tile is at least half of:
+rounding to half of the last bit, or 1 to the largest number below it, leaves at most 2^-28 (2^-24) and so 2^-27
+(2^-23) of the tile's largest, times the rows' codes."""
 import numpy as np
 import pytest
 import torch
