@@ -57,111 +57,129 @@ struct AppendArgs {
   const int32_t* lens;
   const int32_t* counts;
   int64_t n_new, row_stride, batch_stride, capacity;
-  int Hkv, hd, block, nb;  // nb: blocks that n_new rows can touch
+  int Hkv, hd, block_log2, nb;  // nb: blocks that n_new rows can touch
+  uint32_t vpr_magic;           // ceil(2^20 / (hd / 16)): exact for the quotients of up to 2048 vectors by up to 16
   int* status;
 };
 
-// Eight elements of a row as f32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf2_to_f2(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+// Sixteen elements of a row as they were loaded, and as f32.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint4 w[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    w[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    w[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+  __device__ __forceinline__ float4 quad(int q) const {  // elements 4 q .. 4 q + 3
+    const uint4& u = w[q >> 1];
+    const float2 a = bf2_to_f2(q & 1 ? u.z : u.x), b = bf2_to_f2(q & 1 ? u.w : u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+template <>
+struct Raw16<float> {
+  float4 w[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ float4 quad(int q) const { return w[q]; }
+};
 
 // One CTA per (sequence, touched block, K or V, head): the new rows of one block
-// are reduced to their largest finite magnitude and rounded; a block that held
-// rows keeps the larger of its scale and the new one, its codes re-rounded when
-// the scale grows.
-template <typename T>
+// are read once, NV groups of sixteen elements a thread, reduced to their largest
+// finite magnitude and rounded; a block that held rows keeps the larger of its
+// scale and the new one, its codes re-rounded when the scale grows.
+template <typename T, int NV>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs a) {
   __shared__ uint32_t s_max[8];
   const int tid = threadIdx.x, nthr = blockDim.x;
-  int64_t i = blockIdx.x;
-  const int h = static_cast<int>(i % a.Hkv);
+  int i = blockIdx.x;
+  const int h = i % a.Hkv;
   i /= a.Hkv;
-  const int kv = static_cast<int>(i & 1);
+  const int kv = i & 1;
   i >>= 1;
-  const int j = static_cast<int>(i % a.nb);
-  const int b = static_cast<int>(i / a.nb);
+  const int j = i % a.nb;
+  const int b = i / a.nb;
   const int64_t len = checked_len(a.lens[b], a.capacity, a.status);
   int64_t count = a.counts ? a.counts[b] : a.n_new;
   if (count < 0 || count > a.n_new || len + count > a.capacity) {
     if (tid == 0) record_status(a.status, kDevInvalid);
     count = max(int64_t(0), min(min(count, a.n_new), a.capacity - len));
   }
-  const int64_t blk = len / a.block + j;
-  const int64_t lo = blk * a.block;
-  const int64_t r0 = max(lo, len), r1 = min(lo + a.block, len + count);
+  const int64_t blk = (len >> a.block_log2) + j;
+  const int64_t lo = blk << a.block_log2;
+  const int64_t r0 = max(lo, len), r1 = min(lo + (1 << a.block_log2), len + count);
   if (r0 >= r1) return;
-  const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
-  const int vpr = a.hd / 8, nv = static_cast<int>(r1 - r0) * vpr;
+  const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h, nblk = a.capacity >> a.block_log2;
+  const int vpr = a.hd / 16, nv = static_cast<int>(r1 - r0) * vpr;
   const T* src = static_cast<const T*>(a.src[kv]) + b * a.batch_stride + (r0 - len) * a.row_stride + h * a.hd;
-  uint8_t* code = a.code[kv] + (unit * a.capacity + r0) * a.hd;
-  uint32_t big = 0;
-  for (int v = tid; v < nv; v += nthr) {
-    float x[8];
-    load8(src + (v / vpr) * a.row_stride + (v % vpr) * 8, x);
+  Raw16<T> raw[NV];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-      big = max(big, m < 0x7F800000u ? m : 0u);
+  for (int k = 0; k < NV; ++k) {
+    const int v = tid + k * nthr;
+    if (v < nv) {
+      const int row = static_cast<int>((static_cast<uint32_t>(v) * a.vpr_magic) >> 20);  // v / vpr
+      raw[k].load(src + row * a.row_stride + (v - row * vpr) * 16);
+    }
+  }
+  float* scale = a.scale[kv] + unit * nblk + blk;
+  const bool started = len > lo;
+  const float was = started ? *scale : 0.f;
+  uint32_t big = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    if (tid + k * nthr >= nv) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 x = raw[k].quad(q);
+      const uint32_t m[4] = {__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu,
+                             __float_as_uint(x.z) & 0x7FFFFFFFu, __float_as_uint(x.w) & 0x7FFFFFFFu};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) big = max(big, m[e] < 0x7F800000u ? m[e] : 0u);
     }
   }
   big = __reduce_max_sync(0xffffffffu, big);
   if ((tid & 31) == 0) s_max[tid >> 5] = big;
   __syncthreads();
   for (int w = 0; w < nthr / 32; ++w) big = max(big, s_max[w]);
-  int e = scale_exp(big);
-  float* scale = a.scale[kv] + unit * (a.capacity / a.block) + blk;
-  const bool started = len > lo;
-  if (started) {
-    const float was = *scale;
-    const float now = fmaxf(was, pow2f(e));
-    if (now > was) {
-      // the block's scale grows: its codes once more, on the new scale
-      const float ratio = was / now;
-      uint2* old = reinterpret_cast<uint2*>(a.code[kv] + (unit * a.capacity + lo) * a.hd);
-      for (int v = tid; v < static_cast<int>(len - lo) * vpr; v += nthr) {
-        const uint2 w = old[v];
-        const uint32_t c[2] = {w.x, w.y};
-        uint32_t o[2];
+  const float now = fmaxf(was, pow2f(scale_exp(big)));
+  if (started && now > was) {
+    // the block's scale grows: its codes once more, on the new scale
+    const float ratio = was / now;
+    uint4* old = reinterpret_cast<uint4*>(a.code[kv] + (unit * a.capacity + lo) * a.hd);
+    for (int v = tid; v < static_cast<int>(len - lo) * vpr; v += nthr) {
+      const uint4 w = old[v];
+      uint32_t c[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 f0 = from_e4m3x2(static_cast<uint16_t>(c[q])), f1 = from_e4m3x2(static_cast<uint16_t>(c[q] >> 16));
-          o[q] = to_e4m3x2(f0.x * ratio, f0.y * ratio) | static_cast<uint32_t>(to_e4m3x2(f1.x * ratio, f1.y * ratio)) << 16;
-        }
-        old[v] = make_uint2(o[0], o[1]);
+      for (int q = 0; q < 4; ++q) {
+        const float2 f0 = from_e4m3x2(static_cast<uint16_t>(c[q])), f1 = from_e4m3x2(static_cast<uint16_t>(c[q] >> 16));
+        c[q] = to_e4m3x2(f0.x * ratio, f0.y * ratio) | static_cast<uint32_t>(to_e4m3x2(f1.x * ratio, f1.y * ratio)) << 16;
       }
+      old[v] = make_uint4(c[0], c[1], c[2], c[3]);
     }
-    e = static_cast<int>(__float_as_uint(now) >> 23) - 127;
-    __syncthreads();  // every thread has read the old scale
   }
-  const float inv = pow2f(-e);
-  for (int v = tid; v < nv; v += nthr) {
-    float x[8];
-    load8(src + (v / vpr) * a.row_stride + (v % vpr) * 8, x);
-    uint32_t o[2];
+  const float inv = pow2f(127 - static_cast<int>(__float_as_uint(now) >> 23));
+  uint4* code = reinterpret_cast<uint4*>(a.code[kv] + (unit * a.capacity + r0) * a.hd);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      o[q] = to_e4m3x2(x[4 * q] * inv, x[4 * q + 1] * inv) |
-             static_cast<uint32_t>(to_e4m3x2(x[4 * q + 2] * inv, x[4 * q + 3] * inv)) << 16;
-    reinterpret_cast<uint2*>(code)[v] = make_uint2(o[0], o[1]);
+  for (int k = 0; k < NV; ++k) {
+    const int v = tid + k * nthr;
+    if (v >= nv) continue;
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 x = raw[k].quad(q);
+      o[q] = to_e4m3x2(x.x * inv, x.y * inv) | static_cast<uint32_t>(to_e4m3x2(x.z * inv, x.w * inv)) << 16;
+    }
+    code[v] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   if (tid == 0) {
-    *scale = pow2f(e);
+    *scale = now;
     if (kv == 0 && !started) {
       // a block opened by this call: no attention yet, and the next number
-      const int64_t nblk = a.capacity / a.block, held = (len + a.block - 1) / a.block;
+      const int64_t held = (len + (1 << a.block_log2) - 1) >> a.block_log2;
       if (a.weight) a.weight[unit * nblk + blk] = 0.f;
       if (a.ids) a.ids[unit * nblk + blk] = (held ? a.ids[unit * nblk + held - 1] + 1 : 0) + static_cast<int32_t>(blk - held);
     }
@@ -213,17 +231,21 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) {
   return static_cast<int>((checked_len(a.lens[b], a.capacity, a.status) + kTile - 1) / kTile);
 }
 
-// By one warp: the number of tiles before sequence b0 (of its heads), and in all.
-// With x >= 0: finds the sequence whose tiles hold x instead.
+// By one warp: the tiles in all, and a place in their line: sequence b and the
+// tiles before it.  `place` turns the total into the tile looked for, or into
+// -1 - b where a sequence b is; the last sequence has no tile behind it and a
+// tile past the end is at b = B.
 struct Line {
   int before, total, b;
 };
-__device__ inline Line walk_line(const AttendArgs& a, int b0, int x) {
+template <typename F>
+__device__ inline Line walk_line(const AttendArgs& a, F place) {
   const int lane = threadIdx.x & 31;
   Line r{0, 0, a.B};
-  bool found = false;
-  for (int base = 0; base < a.B; base += 256) {
-    int n[8], sum = 0;
+  int n[8], at = 0;
+  // tiles of sequences base + 8 lane ..., and those before them from `carry` on
+  auto load = [&](int base, int carry) {
+    int sum = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int b = base + lane * 8 + k;
@@ -237,25 +259,30 @@ __device__ inline Line walk_line(const AttendArgs& a, int b0, int x) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    int at = r.total + inc - sum;
-    int hit_b = -1, hit_at = 0;
+    at = carry + inc - sum;
+    return carry + __shfl_sync(0xffffffffu, inc, 31);
+  };
+  for (int base = 0; base < a.B; base += 256) r.total = load(base, r.total);
+  const int x = place(r.total);
+  for (int base = 0, carry = 0; base < a.B; base += 256) {
+    if (a.B > 256) carry = load(base, carry);  // else what was loaded still stands
+    int hit_b = -1, hit_at = 0, p = at;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int b = base + lane * 8 + k;
-      if (x >= 0 ? (x >= at && x < at + n[k]) : b == b0) {
+      if (x >= 0 ? (x >= p && x < p + n[k]) : b == -1 - x) {
         hit_b = b;
-        hit_at = at;
+        hit_at = p;
       }
-      at += n[k];
+      p += n[k];
     }
     const unsigned hit = __ballot_sync(0xffffffffu, hit_b >= 0);
-    if (hit && !found) {
+    if (hit) {
       const int src = __ffs(hit) - 1;
       r.b = __shfl_sync(0xffffffffu, hit_b, src);
       r.before = __shfl_sync(0xffffffffu, hit_at, src);
-      found = true;
+      break;
     }
-    r.total += __shfl_sync(0xffffffffu, inc, 31);
   }
   return r;
 }
@@ -327,10 +354,19 @@ struct Pieces;
 template <>
 struct Pieces<__nv_bfloat16> {
   static constexpr int n = 2;
+  using raw = uint2;  // four elements
+  __device__ static __forceinline__ void open(uint2 w, float* v) {
+    const float2 a = bf2_to_f2(w.x), b = bf2_to_f2(w.y);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
 };
 template <>
 struct Pieces<float> {
   static constexpr int n = 6;
+  using raw = float4;
+  __device__ static __forceinline__ void open(float4 w, float* v) {
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
 };
 
 // warps 0-7: softmax, two warpgroups taking tiles in turn
@@ -470,16 +506,14 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     prefetch_tmap(&map_v);
   }
   if (warp == 0) {
-    Line l = walk_line(a, 0, -1);
-    const int total = l.total;
-    const Share s = share_of(total, a.ctas, blockIdx.x);
-    if (s.lo < s.hi) l = walk_line(a, 0, s.lo);
+    const Line l = walk_line(a, [&](int total) { return share_of(total, a.ctas, blockIdx.x).lo; });
     if (lane == 0) {
-      s_total = total;
+      s_total = l.total;
       s_before = l.before;
       s_b = l.b;
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end itself
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -597,36 +631,61 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     } else if (warp == kWarpQ) {
       // queries of one unit: pieces, K-major rows piece * GQ + g, zero past head_dim and past the group
       int seg = 0;
+      const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
       for (int i = 0; i < n;) {
         const int qb = seg % kAhead;
         if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
         const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
-        for (int g = 0; g < GQ; ++g) {
-          const T* q = static_cast<const T*>(a.q) + (unit * a.gq + g) * a.hd;
-          float x[4 * HDA];
-          uint32_t big = 0;
+        // a lane has four columns of every 128; eight heads' loads are in flight at a time
+        constexpr int kBatch = GQ < 8 ? GQ : 8;
 #pragma unroll
-          for (int k = 0; k < 4 * HDA; ++k) {
-            const int j = k * 32 + lane;
-            x[k] = g < a.gq && j < a.hd ? to_f(q[j]) : 0.f;
-            const uint32_t m = __float_as_uint(x[k]) & 0x7FFFFFFFu;
-            big = max(big, m < 0x7F800000u ? m : 0u);
-          }
-          const int e = scale_exp(__reduce_max_sync(0xffffffffu, big));
-          const float inv = pow2f(-e);
+        for (int g0 = 0; g0 < GQ; g0 += kBatch) {
+          typename Pieces<T>::raw raw[kBatch][HDA];
 #pragma unroll
-          for (int k = 0; k < 4 * HDA; ++k) {
-            const int j = k * 32 + lane;
-            // what is not finite makes the head's logits NaN
-            float r = (__float_as_uint(x[k]) & 0x7FFFFFFFu) < 0x7F800000u ? x[k] * inv : __uint_as_float(0x7FC00000u);
+          for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-            for (int p = 0; p < kNq; ++p) {
-              const uint16_t c = to_e4m3x2(r, 0.f);
-              r = 16.f * (r - from_e4m3x2(c).x);
-              sq[(qb * HDA + (j >> 7)) * Sh::ns * 128 + swz128(p * GQ + g, j & 127)] = static_cast<uint8_t>(c);
+            for (int x = 0; x < HDA; ++x) {
+              const int j = 128 * x + 4 * lane;
+              raw[k][x] = typename Pieces<T>::raw{};
+              if (g0 + k < a.gq && j < a.hd)
+                raw[k][x] = *reinterpret_cast<const typename Pieces<T>::raw*>(
+                    static_cast<const T*>(a.q) + (unit * a.gq + g0 + k) * a.hd + j);
             }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int g = g0 + k;
+            float v[HDA][4];
+            uint32_t big = 0;
+#pragma unroll
+            for (int x = 0; x < HDA; ++x) {
+              Pieces<T>::open(raw[k][x], v[x]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m = __float_as_uint(v[x][e]) & 0x7FFFFFFFu;
+                if (m < 0x7F800000u) big = max(big, m);
+                else v[x][e] = __uint_as_float(0x7FC00000u);  // what is not finite makes the head's logits NaN
+              }
+            }
+            const int e2 = scale_exp(__reduce_max_sync(0xffffffffu, big));
+            const float inv = pow2f(-e2);
+#pragma unroll
+            for (int x = 0; x < HDA; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[x][e] *= inv;
+#pragma unroll
+              for (int p = 0; p < kNq; ++p) {
+                const uint16_t c0 = to_e4m3x2(v[x][0], v[x][1]), c1 = to_e4m3x2(v[x][2], v[x][3]);
+                const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
+                v[x][0] = 16.f * (v[x][0] - f0.x);
+                v[x][1] = 16.f * (v[x][1] - f0.y);
+                v[x][2] = 16.f * (v[x][2] - f1.x);
+                v[x][3] = 16.f * (v[x][3] - f1.y);
+                *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g, 4 * lane)) =
+                    c0 | static_cast<uint32_t>(c1) << 16;
+              }
+            }
+            if (lane == 0) s_qc[qb][g] = pow2f(e2) * q_scale;
           }
-          if (lane == 0) s_qc[qb][g] = pow2f(e) * (kLog2e / sqrtf(static_cast<float>(a.hd)));
         }
         fence_proxy_async();
         mbar_arrive(&q_full[qb]);
@@ -849,7 +908,10 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 
 // Joins a unit's partials: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
 // CTA (unit, y < gq) writes head y's output, warp by slot; CTAs (unit, y >= gq)
-// add a share of the blocks' weights, sum_g 2^(ref - M_g) wpart / L_g.
+// add a share of the blocks' weights, sum_g 2^(ref - M_g) wpart / L_g.  What it
+// costs is latency, so every thread has its loads in flight together, and the
+// launch is a programmatic one: its CTAs find their unit while the attention
+// still runs.
 constexpr int kCombineThreads = 256;
 constexpr int kMaxSlots = 2 * 256;  // of one unit: two for each CTA
 
@@ -860,7 +922,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
   const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == 0) {
-    const Line l = walk_line(a, b, -1);
+    const Line l = walk_line(a, [&](int) { return -1 - b; });
     if (lane == 0) {
       s_before = l.before;
       s_total = l.total;
@@ -868,6 +930,9 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
   }
   __syncthreads();
   const int nt = tiles_of(a, b);
+  const int x0 = s_before + h * nt, x1 = x0 + nt;
+  const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x1 - 1) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's partials from here on
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
     if (static_cast<int>(blockIdx.y) < gq)
@@ -876,32 +941,44 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
   }
   // the slots of the unit: each CTA whose share meets it left one for each
   // warpgroup that had a tile of it
-  const int x0 = s_before + h * nt, x1 = x0 + nt;
-  const int c0 = cta_of(s_total, a.ctas, x0), c1 = cta_of(s_total, a.ctas, x1 - 1);
   const int sf = slot_floats(gq, hd), slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
   auto written = [&](int k) {
     const Share sh = share_of(s_total, a.ctas, c0 + k / 2);
     const int lo = max(sh.lo, x0), hi = min(sh.hi, x1);
-    return hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1);
+    return k < slots && (hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1));
   };
   // by one warp: head g's largest reference and sum, and (factors) every slot's 2^(m - M) into s_f
   auto head = [&](int g, bool factors) {
-    float M = -INFINITY;
-    for (int k = lane; k < slots; k += 32)
-      if (written(k)) M = fmaxf(M, base[static_cast<int64_t>(k) * sf + gq * hd + g]);
-    M = warp_max(M);
-    float L = 0.f;
-    for (int k = lane; k < slots; k += 32) {
-      float f = 0.f;
-      if (written(k)) {
+    constexpr int kHeld = 4;  // slots a lane holds: 128 in all, the rest in further rounds
+    float M = -INFINITY, L = 0.f;
+    for (int base_k = 0; base_k < slots; base_k += 32 * kHeld) {
+      float m[kHeld], l[kHeld];
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) {
+        const int k = base_k + 32 * e + lane;
         const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + g;
-        f = s[0] == M ? 1.f : exp2f(s[0] - M);
-        L += s[gq] * f;
+        const bool w = written(k);
+        m[e] = w ? s[0] : -INFINITY;
+        l[e] = w ? s[gq] : 0.f;
       }
-      if (factors) s_f[k] = f;
+      float top = M;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) top = fmaxf(top, m[e]);
+      top = warp_max(top);
+      if (top != M) L *= exp2f(M - top);
+      M = top;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e)
+        // references are equal where all logits of a unit are NaN (then -inf) or by chance
+        if (l[e] != 0.f) L += l[e] * (m[e] == M ? 1.f : exp2f(m[e] - M));
     }
     L = warp_sum(L);
+    if (factors)
+      for (int k = lane; k < slots; k += 32) {
+        const float m = written(k) ? base[static_cast<int64_t>(k) * sf + gq * hd + g] : -INFINITY;
+        s_f[k] = !written(k) ? 0.f : m == M ? 1.f : exp2f(m - M);
+      }
     if (lane == 0) {
       s_m[g] = M;
       s_r[g] = 1.f / L;
@@ -911,29 +988,26 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
     const int g = blockIdx.y;
     if (warp == 0) head(g, true);
     __syncthreads();
-    float acc[8];
+    float2 acc[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-    const int per = hd / 16;  // columns in pairs: lane and 16-column steps
+    for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+    const int pairs = hd / 2;  // a lane's columns come in pairs, 64 columns apart
+#pragma unroll 4
     for (int k = warp; k < slots; k += 8) {
       const float f = s_f[k];
       const float2* s = reinterpret_cast<const float2*>(base + static_cast<int64_t>(k) * sf + g * hd);
-      // an unwritten slot holds anything
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int col = e * 32 + lane;
-        if (col < per * 8) {
-          const float2 v = f != 0.f ? s[col] : make_float2(0.f, 0.f);
-          acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
-          acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
-        }
+        // an unwritten slot holds anything
+        const float2 v = f != 0.f && col < pairs ? s[col] : make_float2(0.f, 0.f);
+        acc[e].x = fmaf(f, v.x, acc[e].x);
+        acc[e].y = fmaf(f, v.y, acc[e].y);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int col = e * 32 + lane;
-      if (col < per * 8) *reinterpret_cast<float2*>(&s_red[warp][2 * col]) = make_float2(acc[2 * e], acc[2 * e + 1]);
-    }
+    for (int e = 0; e < 4; ++e)
+      if (e * 32 + lane < pairs) *reinterpret_cast<float2*>(&s_red[warp][2 * (e * 32 + lane)]) = acc[e];
     __syncthreads();
     if (tid < hd) {
       float o = 0.f;
@@ -949,15 +1023,22 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
   const int n = static_cast<int>((checked_len(a.lens[b], a.capacity, nullptr) + a.block - 1) / a.block);
   const int sub = sub_rows(a.block), spb = a.block / sub, spt = kTile / sub;
   for (int k = (blockIdx.y - gq) * kCombineThreads + tid; k < n; k += (gridDim.y - gq) * kCombineThreads) {
-    float w = 0.f;
     const int64_t s0 = static_cast<int64_t>(k) * spb, tile = s0 / spt;
     const float* ref = a.wref + (static_cast<int64_t>(unit) * a.tiles_cap + tile) * gq;
     const float* p = a.wpart + (static_cast<int64_t>(unit) * a.tiles_cap * spt + s0) * gq;
-#pragma unroll 4
-    for (int g = 0; g < gq; ++g) {
-      float s = p[g];
-      for (int e = 1; e < spb; ++e) s += p[e * gq + g];
-      w = fmaf(s, exp2f(ref[g] - s_m[g]) * s_r[g], w);
+    float w = 0.f;
+    for (int g0 = 0; g0 < gq; g0 += 4) {
+      float r[4], v[4][4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const bool in = g0 + g < gq;
+        r[g] = in ? ref[g0 + g] - s_m[g0 + g] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[g][e] = in && e < spb ? p[e * gq + g0 + g] : 0.f;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g0 + g < gq) w = fmaf((v[g][0] + v[g][1]) + (v[g][2] + v[g][3]), exp2f(r[g]) * s_r[g0 + g], w);
     }
     a.weight[unit * nblk + k] += w;
   }
@@ -1149,35 +1230,52 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   int* pref_f = reinterpret_cast<int*>(equal);
   const int moves = block_scan(nw, pref_m, s_warp, [&](int w) { return __popc(mover(w)); });
   block_scan(we + 1, pref_f, s_warp, [&](int w) { return __popc(empty(w)); });
-  const int nv = a.block * a.hd / 16;
-  auto move = [&](int r, int first, int step) {
+  // The moves' bytes in pieces of 32 x 8 vectors, dealt out to the cluster's warps: a warp has a piece's
+  // loads in flight together.
+  const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
+  auto move = [&](int r, int x, int piece) __attribute__((always_inline)) {
     const int wm = find_word(pref_m, 0, nw, r), wf = find_word(pref_f, 0, we + 1, r);
     const int64_t src = wm * 32 + nth_bit(mover(wm), r - pref_m[wm]);
     const int64_t dst = wf * 32 + nth_bit(empty(wf), r - pref_f[wf]);
+    const uint4* from = reinterpret_cast<const uint4*>(a.code[x] + (unit * a.capacity + src * a.block) * a.hd);
+    uint4* to = reinterpret_cast<uint4*>(a.code[x] + (unit * a.capacity + dst * a.block) * a.hd);
+    uint4 v[8];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint4* from = reinterpret_cast<const uint4*>(a.code[x] + (unit * a.capacity + src * a.block) * a.hd);
-      uint4* to = reinterpret_cast<uint4*>(a.code[x] + (unit * a.capacity + dst * a.block) * a.hd);
-#pragma unroll 8
-      for (int v = first; v < nv; v += step) to[v] = from[v];
-    }
-    if (first == 0) {
+    for (int k = 0; k < 8; ++k)
+      if (piece * 256 + k * 32 + lane < nv) v[k] = from[piece * 256 + k * 32 + lane];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (piece * 256 + k * 32 + lane < nv) to[piece * 256 + k * 32 + lane] = v[k];
+    if (piece == 0 && lane == 0) {
       const int64_t o = unit * nblk;
-      a.scale[0][o + dst] = a.scale[0][o + src];
-      a.scale[1][o + dst] = a.scale[1][o + src];
-      a.weight[o + dst] = a.weight[o + src];
-      a.ids[o + dst] = a.ids[o + src];
+      a.scale[x][o + dst] = a.scale[x][o + src];
+      if (x == 0) a.weight[o + dst] = a.weight[o + src];
+      else a.ids[o + dst] = a.ids[o + src];
     }
   };
-  for (int r = warp * kEvictCtas + rank; r < moves - 1; r += kEvictCtas * kEvictThreads / 32) move(r, lane, 32);
+  constexpr int kWarps = kEvictCtas * kEvictThreads / 32;
+  for (int64_t w = warp * kEvictCtas + rank; w < static_cast<int64_t>(moves - 1) * 2 * per; w += kWarps)
+    move(static_cast<int>(w / (2 * per)), static_cast<int>(w / per) & 1, static_cast<int>(w % per));
   cluster_sync();  // slot budget - 1 has been read
-  if (rank == 0) move(moves - 1, tid, kEvictThreads);
+  for (int w = warp * kEvictCtas + rank; w < 2 * per; w += kWarps) move(moves - 1, w / per, w % per);
   if (writes_len) a.lens_out[b] = static_cast<int32_t>(len - static_cast<int64_t>(n - a.budget) * a.block);
 }
 
 }  // namespace
 
 // -------------------------------------------------------------- launchers
+// Threads and vectors a thread for the rows one block can get: 128 threads up to
+// four vectors each (64 rows of 128), 256 for more.
+template <typename T>
+static void append_typed(const AppendArgs& a, int64_t n_new, int block, unsigned grid, cudaStream_t st) {
+  const int vecs = static_cast<int>(std::min<int64_t>(n_new, block)) * a.hd / 16;
+  if (vecs <= 128) kv8_append_kernel<T, 1><<<grid, 128, 0, st>>>(a);
+  else if (vecs <= 256) kv8_append_kernel<T, 2><<<grid, 128, 0, st>>>(a);
+  else if (vecs <= 512) kv8_append_kernel<T, 4><<<grid, 128, 0, st>>>(a);
+  else if (vecs <= 1024) kv8_append_kernel<T, 4><<<grid, 256, 0, st>>>(a);
+  else kv8_append_kernel<T, 8><<<grid, 256, 0, st>>>(a);
+}
+
 xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens,
                              const int32_t* counts, int64_t n_new, xkv_dtype dt, const void* k_new, const void* v_new,
                              int64_t row_stride, int64_t batch_stride, cudaStream_t st) {
@@ -1198,18 +1296,15 @@ xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   a.capacity = p->capacity;
   a.Hkv = p->n_kv_heads;
   a.hd = p->head_dim;
-  a.block = p->block;
+  a.block_log2 = 31 - __builtin_clz(static_cast<unsigned>(p->block));
+  a.vpr_magic = static_cast<uint32_t>(((1 << 20) + p->head_dim / 16 - 1) / (p->head_dim / 16));
   const int64_t nb = (n_new + p->block - 2) / p->block + 1;
   a.nb = static_cast<int>(std::min(nb, p->capacity / p->block));
   a.status = device_status_ptr();
   const int64_t grid = static_cast<int64_t>(p->batch) * p->n_kv_heads * 2 * a.nb;
   if (grid > 0x7FFFFFFF) return XKV_ERR_UNSUPPORTED;
-  const int64_t vecs = std::min<int64_t>(n_new, p->block) * p->head_dim / 8;
-  const int threads = vecs <= 128 ? 128 : 256;
-  if (dt == XKV_BF16)
-    kv8_append_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), threads, 0, st>>>(a);
-  else
-    kv8_append_kernel<float><<<static_cast<unsigned>(grid), threads, 0, st>>>(a);
+  if (dt == XKV_BF16) append_typed<__nv_bfloat16>(a, n_new, p->block, static_cast<unsigned>(grid), st);
+  else append_typed<float>(a, n_new, p->block, static_cast<unsigned>(grid), st);
   return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
 }
 
@@ -1292,7 +1387,16 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
     const int64_t nblk = p->capacity / p->block;
     wy = static_cast<int>(std::min<int64_t>((nblk + kCombineThreads - 1) / kCombineThreads, 64));
   }
-  kv8_combine_kernel<<<dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads, a.gq + wy), kCombineThreads, 0, st>>>(a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads, a.gq + wy);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv8_combine_kernel, a) != cudaSuccess) return XKV_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
 }
 
