@@ -194,7 +194,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> C.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 

@@ -194,7 +194,7 @@ struct AttendArgs {
   const float* v_scale;
   const void* q;
   const int32_t* lens;
-  float* part;   // partial slots: [gq][hd] sums, [gq] maxima, [gq] softmax sums
+  float* part;   // partial slots: [gq][hd] sums, [gq] references, [4][gq] softmax sums of a warp's rows
   float* wpart;  // [unit][tile][sub-block][gq] sums of the tile's weights, or NULL
   float* wref;   // [unit][tile][gq] the maxima they refer to
   float* weight;
@@ -205,7 +205,8 @@ struct AttendArgs {
   int* status;
 };
 
-__host__ __device__ inline int slot_floats(int gq, int hd) { return gq * (hd + 2); }
+// a multiple of four, so that a slot's columns can be read in pairs
+__host__ __device__ inline int slot_floats(int gq, int hd) { return (gq * (hd + 5) + 3) & ~3; }
 __host__ __device__ inline int sub_rows(int block) { return block < 32 ? block : 32; }
 
 // Units' tiles stand in one line (sequence, head, tile), and CTA c of n takes a
@@ -471,7 +472,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ int s_abort, s_total, s_before, s_b;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
-  __shared__ float s_sum[2][4][GQ], s_qc[kAhead][GQ];
+  __shared__ float s_qc[kAhead][GQ];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sm;
   uint8_t* sv = sk + kStages * HDA * kAtom;
@@ -651,41 +652,54 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 raw[k][x] = *reinterpret_cast<const typename Pieces<T>::raw*>(
                     static_cast<const T*>(a.q) + (unit * a.gq + g0 + k) * a.hd + j);
             }
+          // step by step over the batch, so that no step waits for one head's chain
+          float v[kBatch][HDA][4];
+          uint32_t big[kBatch];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const int g = g0 + k;
-            float v[HDA][4];
-            uint32_t big = 0;
+            big[k] = 0;
 #pragma unroll
             for (int x = 0; x < HDA; ++x) {
-              Pieces<T>::open(raw[k][x], v[x]);
+              Pieces<T>::open(raw[k][x], v[k][x]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t m = __float_as_uint(v[x][e]) & 0x7FFFFFFFu;
-                if (m < 0x7F800000u) big = max(big, m);
-                else v[x][e] = __uint_as_float(0x7FC00000u);  // what is not finite makes the head's logits NaN
+                const uint32_t m = __float_as_uint(v[k][x][e]) & 0x7FFFFFFFu;
+                const bool finite = m < 0x7F800000u;
+                big[k] = max(big[k], finite ? m : 0u);
+                v[k][x][e] = finite ? v[k][x][e] : __uint_as_float(0x7FC00000u);  // makes the head's logits NaN
               }
             }
-            const int e2 = scale_exp(__reduce_max_sync(0xffffffffu, big));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) big[k] = __reduce_max_sync(0xffffffffu, big[k]);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int e2 = scale_exp(big[k]);
             const float inv = pow2f(-e2);
 #pragma unroll
-            for (int x = 0; x < HDA; ++x) {
+            for (int x = 0; x < HDA; ++x)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[x][e] *= inv;
-#pragma unroll
-              for (int p = 0; p < kNq; ++p) {
-                const uint16_t c0 = to_e4m3x2(v[x][0], v[x][1]), c1 = to_e4m3x2(v[x][2], v[x][3]);
-                const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
-                v[x][0] = 16.f * (v[x][0] - f0.x);
-                v[x][1] = 16.f * (v[x][1] - f0.y);
-                v[x][2] = 16.f * (v[x][2] - f1.x);
-                v[x][3] = 16.f * (v[x][3] - f1.y);
-                *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g, 4 * lane)) =
-                    c0 | static_cast<uint32_t>(c1) << 16;
-              }
-            }
-            if (lane == 0) s_qc[qb][g] = pow2f(e2) * q_scale;
+              for (int e = 0; e < 4; ++e) v[k][x][e] *= inv;
+            if (lane == 0) s_qc[qb][g0 + k] = pow2f(e2) * q_scale;
           }
+#pragma unroll
+          for (int p = 0; p < kNq; ++p)
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+              for (int x = 0; x < HDA; ++x) {
+                float* r = v[k][x];
+                const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
+                *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g0 + k, 4 * lane)) =
+                    c0 | static_cast<uint32_t>(c1) << 16;
+                if (p + 1 < kNq) {
+                  const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
+                  r[0] = 16.f * (r[0] - f0.x);
+                  r[1] = 16.f * (r[1] - f0.y);
+                  r[2] = 16.f * (r[2] - f1.x);
+                  r[3] = 16.f * (r[3] - f1.y);
+                }
+              }
         }
         fence_proxy_async();
         mbar_arrive(&q_full[qb]);
@@ -878,19 +892,15 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           fold(((i1 - 1 - wg) & ~1) / 2);
           float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * slot_floats(a.gq, a.hd);
 #pragma unroll
-          for (int g = 0; g < GQ; ++g) {
-            const float sum = warp_sum(l[g]);
-            if (lane == 0) s_sum[wg][quarter][g] = sum;
+          for (int g = 0; g < GQ; ++g)
 #pragma unroll
             for (int x = 0; x < HDA; ++x)
               if (g < a.gq && row + 128 * x < a.hd) slot[g * a.hd + row + 128 * x] = acc[x][g];
-          }
-          named_bar_sync(1 + wg, 128);
-          if (row < a.gq) {
-            slot[a.gq * a.hd + row] = m;
-            slot[a.gq * a.hd + a.gq + row] = s_sum[wg][0][row] + s_sum[wg][1][row] + s_sum[wg][2][row] + s_sum[wg][3][row];
-          }
-          named_bar_sync(1 + wg, 128);
+          slot += a.gq * a.hd;
+          group_sums<GQ>(l, 32, [&](int g, float sum) {
+            if (g < a.gq) slot[(1 + quarter) * a.gq + g] = sum;
+          });
+          if (row < a.gq) slot[row] = m;
         }
         // to the next unit
         i0 = i1;
@@ -907,18 +917,20 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 }
 
 // Joins a unit's partials: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
-// CTA (unit, y < gq) writes head y's output, warp by slot; CTAs (unit, y >= gq)
-// add a share of the blocks' weights, sum_g 2^(ref - M_g) wpart / L_g.  What it
-// costs is latency, so every thread has its loads in flight together, and the
-// launch is a programmatic one: its CTAs find their unit while the attention
-// still runs.
+// CTA (unit, y) takes `heads` (1, 2, 4 or 8) query heads, each by 8 / heads warps,
+// a warp by slot; CTAs (unit, y >= head_ctas) add a share of the blocks' weights,
+// sum_g 2^(ref - M_g) wpart / L_g.  What it costs is latency, so every thread has
+// its loads in flight together, one CTA takes several heads where there are
+// units enough, and the launch is a programmatic one: its CTAs find their unit
+// while the attention still runs.
 constexpr int kCombineThreads = 256;
 constexpr int kMaxSlots = 2 * 256;  // of one unit: two for each CTA
 
-__global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const AttendArgs a, int heads, int head_ctas) {
   __shared__ int s_before, s_total;
-  __shared__ float s_f[kMaxSlots];
-  __shared__ float s_m[16], s_r[16], s_red[8][256];
+  __shared__ float s_f[8][kMaxSlots];
+  __shared__ float s_m[16], s_r[16];
+  __shared__ __align__(8) float s_red[8][256];
   const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == 0) {
@@ -928,15 +940,16 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
       s_total = l.total;
     }
   }
+  const int64_t len = checked_len(a.lens[b], a.capacity, nullptr);
+  const int nt = static_cast<int>((len + kTile - 1) / kTile);
   __syncthreads();
-  const int nt = tiles_of(a, b);
-  const int x0 = s_before + h * nt, x1 = x0 + nt;
-  const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x1 - 1) : 0;
+  const int x0 = s_before + h * nt, x1 = x0 + nt, total = s_total;
+  const int c0 = nt ? cta_of(total, a.ctas, x0) : 0, c1 = nt ? cta_of(total, a.ctas, x1 - 1) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's partials from here on
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
-    if (static_cast<int>(blockIdx.y) < gq)
-      for (int i = tid; i < hd; i += kCombineThreads) out[blockIdx.y * hd + i] = 0.f;
+    if (blockIdx.y == 0)
+      for (int i = tid; i < gq * hd; i += kCombineThreads) out[i] = 0.f;
     return;
   }
   // the slots of the unit: each CTA whose share meets it left one for each
@@ -944,23 +957,24 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
   const int sf = slot_floats(gq, hd), slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
   auto written = [&](int k) {
-    const Share sh = share_of(s_total, a.ctas, c0 + k / 2);
+    const Share sh = share_of(total, a.ctas, c0 + k / 2);
     const int lo = max(sh.lo, x0), hi = min(sh.hi, x1);
     return k < slots && (hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1));
   };
-  // by one warp: head g's largest reference and sum, and (factors) every slot's 2^(m - M) into s_f
-  auto head = [&](int g, bool factors) {
-    constexpr int kHeld = 4;  // slots a lane holds: 128 in all, the rest in further rounds
+  // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M)
+  auto head = [&](int g, float* f) {
+    constexpr int kHeld = 2;  // slots a lane holds: 64 in all, the rest in further rounds
     float M = -INFINITY, L = 0.f;
-    for (int base_k = 0; base_k < slots; base_k += 32 * kHeld) {
+    for (int from = 0; from < slots; from += 32 * kHeld) {
       float m[kHeld], l[kHeld];
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) {
-        const int k = base_k + 32 * e + lane;
+        const int k = from + 32 * e + lane;
         const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + g;
         const bool w = written(k);
         m[e] = w ? s[0] : -INFINITY;
-        l[e] = w ? s[gq] : 0.f;
+        l[e] = w ? (s[gq] + s[2 * gq]) + (s[3 * gq] + s[4 * gq]) : 0.f;
+        if (f && k < slots) f[k] = m[e];
       }
       float top = M;
 #pragma unroll
@@ -970,63 +984,63 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
       M = top;
 #pragma unroll
       for (int e = 0; e < kHeld; ++e)
-        // references are equal where all logits of a unit are NaN (then -inf) or by chance
-        if (l[e] != 0.f) L += l[e] * (m[e] == M ? 1.f : exp2f(m[e] - M));
+        if (l[e] != 0.f) L += l[e] * (m[e] == M ? 1.f : exp2f(m[e] - M));  // all NaN: m = M = -inf
     }
     L = warp_sum(L);
-    if (factors)
-      for (int k = lane; k < slots; k += 32) {
-        const float m = written(k) ? base[static_cast<int64_t>(k) * sf + gq * hd + g] : -INFINITY;
-        s_f[k] = !written(k) ? 0.f : m == M ? 1.f : exp2f(m - M);
-      }
+    if (f)
+      for (int k = lane; k < slots; k += 32) f[k] = !written(k) ? 0.f : f[k] == M ? 1.f : exp2f(f[k] - M);
     if (lane == 0) {
       s_m[g] = M;
       s_r[g] = 1.f / L;
     }
   };
-  if (static_cast<int>(blockIdx.y) < gq) {
-    const int g = blockIdx.y;
-    if (warp == 0) head(g, true);
+  if (static_cast<int>(blockIdx.y) < head_ctas) {
+    const int wph = 8 / heads, slot = warp / wph, part = warp % wph, g = blockIdx.y * heads + slot;
+    if (part == 0 && g < gq) head(g, s_f[slot]);
     __syncthreads();
-    float2 acc[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
     const int pairs = hd / 2;  // a lane's columns come in pairs, 64 columns apart
+    if (g < gq) {
+      float2 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int k = warp; k < slots; k += 8) {
-      const float f = s_f[k];
-      const float2* s = reinterpret_cast<const float2*>(base + static_cast<int64_t>(k) * sf + g * hd);
+      for (int k = part; k < slots; k += wph) {
+        const float f = s_f[slot][k];
+        const float2* s = reinterpret_cast<const float2*>(base + static_cast<int64_t>(k) * sf + g * hd);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = e * 32 + lane;
-        // an unwritten slot holds anything
-        const float2 v = f != 0.f && col < pairs ? s[col] : make_float2(0.f, 0.f);
-        acc[e].x = fmaf(f, v.x, acc[e].x);
-        acc[e].y = fmaf(f, v.y, acc[e].y);
+        for (int e = 0; e < 4; ++e) {
+          const int col = e * 32 + lane;
+          // an unwritten slot holds anything
+          const float2 v = f != 0.f && col < pairs ? s[col] : make_float2(0.f, 0.f);
+          acc[e].x = fmaf(f, v.x, acc[e].x);
+          acc[e].y = fmaf(f, v.y, acc[e].y);
+        }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e * 32 + lane < pairs) *reinterpret_cast<float2*>(&s_red[warp][2 * (e * 32 + lane)]) = acc[e];
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e * 32 + lane < pairs) *reinterpret_cast<float2*>(&s_red[warp][2 * (e * 32 + lane)]) = acc[e];
     __syncthreads();
-    if (tid < hd) {
+    for (int i = tid; i < heads * hd; i += kCombineThreads) {
+      const int hh = i / hd, col = i % hd, gg = blockIdx.y * heads + hh;
+      if (gg >= gq) break;
       float o = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o += s_red[k][tid];
-      out[g * hd + tid] = o * s_r[g];
+      for (int k = 0; k < wph; ++k) o += s_red[hh * wph + k][col];
+      out[gg * hd + col] = o * s_r[gg];
     }
     return;
   }
-  for (int g = warp; g < gq; g += 8) head(g, false);
+  for (int g = warp; g < gq; g += 8) head(g, nullptr);
   __syncthreads();
   const int64_t nblk = a.capacity / a.block;
-  const int n = static_cast<int>((checked_len(a.lens[b], a.capacity, nullptr) + a.block - 1) / a.block);
+  const int n = static_cast<int>((len + a.block - 1) / a.block);
   const int sub = sub_rows(a.block), spb = a.block / sub, spt = kTile / sub;
-  for (int k = (blockIdx.y - gq) * kCombineThreads + tid; k < n; k += (gridDim.y - gq) * kCombineThreads) {
+  const int share = gridDim.y - head_ctas;
+  for (int k = (blockIdx.y - head_ctas) * kCombineThreads + tid; k < n; k += share * kCombineThreads) {
     const int64_t s0 = static_cast<int64_t>(k) * spb, tile = s0 / spt;
     const float* ref = a.wref + (static_cast<int64_t>(unit) * a.tiles_cap + tile) * gq;
     const float* p = a.wpart + (static_cast<int64_t>(unit) * a.tiles_cap * spt + s0) * gq;
-    float w = 0.f;
+    float w = a.weight[unit * nblk + k], sum = 0.f;
     for (int g0 = 0; g0 < gq; g0 += 4) {
       float r[4], v[4][4];
 #pragma unroll
@@ -1038,9 +1052,9 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const Atte
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        if (g0 + g < gq) w = fmaf((v[g][0] + v[g][1]) + (v[g][2] + v[g][3]), exp2f(r[g]) * s_r[g0 + g], w);
+        if (g0 + g < gq) sum = fmaf((v[g][0] + v[g][1]) + (v[g][2] + v[g][3]), exp2f(r[g]) * s_r[g0 + g], sum);
     }
-    a.weight[unit * nblk + k] += w;
+    a.weight[unit * nblk + k] = w + sum;
   }
 }
 
@@ -1382,13 +1396,18 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   }
   const xkv_status s = dt == XKV_BF16 ? attend_tc<__nv_bfloat16>(a, maps, st) : attend_tc<float>(a, maps, st);
   if (s != XKV_OK) return s;
+  // joining: heads to a CTA so that its grid is about what the card holds at once (four CTAs an SM)
+  const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads;
+  int heads = 1;
+  while (heads < 8 && heads < a.gq && units * ((a.gq + heads - 1) / heads) > 4 * num_sms()) heads *= 2;
+  const int head_ctas = (a.gq + heads - 1) / heads;
   int wy = 0;
   if (accumulate) {
     const int64_t nblk = p->capacity / p->block;
     wy = static_cast<int>(std::min<int64_t>((nblk + kCombineThreads - 1) / kCombineThreads, 64));
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads, a.gq + wy);
+  cfg.gridDim = dim3(static_cast<unsigned>(units), head_ctas + wy);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -1396,7 +1415,7 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv8_combine_kernel, a) != cudaSuccess) return XKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kv8_combine_kernel, a, heads, head_ctas) != cudaSuccess) return XKV_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
 }
 

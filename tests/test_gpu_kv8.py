@@ -205,6 +205,9 @@ def test_append_past_the_capacity_and_bad_lengths(xkv):
     ("f32", 5, 1, 48, 16, [2000, 17, 0, 300]),
     ("bf16", 2, 12, 112, 32, [640]),
     ("bf16", 2, 5, 128, 128, [4, 5000]),
+    ("bf16", 1, 1, 48, 16, [40000, 129]),   # several tiles to a CTA, odd sizes of the partials
+    ("f32", 1, 3, 16, 8, [50001]),
+    ("bf16", 3, 16, 128, 64, [20000, 1]),
 ])
 def test_attention_matches_float64(xkv, dt, H, gq, hd, block, counts):
     B = len(counts)
