@@ -228,9 +228,11 @@ __device__ __forceinline__ int cta_of(int total, int n, int x) {
   return x < cut ? x / (q + 1) : r + (x - cut) / q;
 }
 
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) {
-  return static_cast<int>((checked_len(a.lens[b], a.capacity, a.status) + kTile - 1) / kTile);
+// Rows of sequence b, within the cache (the joining kernel records a length outside), and their tiles.
+__device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {
+  return min(max(a.lens[b], 0), static_cast<int>(a.capacity));
 }
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) { return (rows_of(a, b) + kTile - 1) / kTile; }
 
 // By one warp: the tiles in all, and a place in their line: sequence b and the
 // tiles before it.  `place` turns the total into the tile looked for, or into
@@ -241,19 +243,20 @@ struct Line {
 };
 template <typename F>
 __device__ inline Line walk_line(const AttendArgs& a, F place) {
+  constexpr int kEach = 4;  // sequences a lane takes at a time
   const int lane = threadIdx.x & 31;
   Line r{0, 0, a.B};
-  int n[8], at = 0;
-  // tiles of sequences base + 8 lane ..., and those before them from `carry` on
+  int n[kEach], at = 0;
+  // tiles of sequences base + kEach lane ..., and those before them from `carry` on
   auto load = [&](int base, int carry) {
     int sum = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int b = base + lane * 8 + k;
+    for (int k = 0; k < kEach; ++k) {
+      const int b = base + lane * kEach + k;
       n[k] = b < a.B ? tiles_of(a, b) * a.Hkv : 0;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += n[k];
+    for (int k = 0; k < kEach; ++k) sum += n[k];
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -263,14 +266,14 @@ __device__ inline Line walk_line(const AttendArgs& a, F place) {
     at = carry + inc - sum;
     return carry + __shfl_sync(0xffffffffu, inc, 31);
   };
-  for (int base = 0; base < a.B; base += 256) r.total = load(base, r.total);
+  for (int base = 0; base < a.B; base += 32 * kEach) r.total = load(base, r.total);
   const int x = place(r.total);
-  for (int base = 0, carry = 0; base < a.B; base += 256) {
-    if (a.B > 256) carry = load(base, carry);  // else what was loaded still stands
+  for (int base = 0, carry = 0; base < a.B; base += 32 * kEach) {
+    if (a.B > 32 * kEach) carry = load(base, carry);  // else what was loaded still stands
     int hit_b = -1, hit_at = 0, p = at;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int b = base + lane * 8 + k;
+    for (int k = 0; k < kEach; ++k) {
+      const int b = base + lane * kEach + k;
       if (x >= 0 ? (x >= p && x < p + n[k]) : b == -1 - x) {
         hit_b = b;
         hit_at = p;
@@ -288,18 +291,12 @@ __device__ inline Line walk_line(const AttendArgs& a, F place) {
   return r;
 }
 
-// One role's position in its CTA's share: tile t of unit (b, h).
+// One role's position in its CTA's share: tile t of the nt tiles of unit (b, h).
 struct Walk {
-  int b, h, t, nt;
-  int64_t len;
+  int b, h, t, nt, len;
   __device__ __forceinline__ void load(const AttendArgs& a) {
-    len = checked_len(a.lens[b], a.capacity, nullptr);
-    nt = static_cast<int>((len + kTile - 1) / kTile);
-  }
-  __device__ __forceinline__ Walk(const AttendArgs& a, int first_b, int skip) : b(first_b) {
-    load(a);
-    h = skip / nt;
-    t = skip % nt;
+    len = rows_of(a, b);
+    nt = (len + kTile - 1) / kTile;
   }
   // The next tile; only where there is one.
   __device__ __forceinline__ void step(const AttendArgs& a) {
@@ -453,7 +450,7 @@ __device__ __forceinline__ void group_sums(const float* p, int sub, F f) {
 //                   column of O, which is summed in f32 registers;
 //   warp 8: TMA of the K and V rings; warps 9, 10: the MMAs of S and of O, of
 //   their own so that neither waits for the other's operands; warp 11: the
-//   queries' pieces.
+//   pieces of the next units' queries.
 // Rows behind the sequence's end are masked in S, and their V rows zeroed before
 // the MMA (0 * NaN).
 template <typename T, int GQ, int HDA>
@@ -469,7 +466,9 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ __align__(8) uint64_t s_full[kAhead], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_total, s_before, s_b;
+  __shared__ int s_abort;
+  __shared__ Share s_share;
+  __shared__ Walk s_walk;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
   __shared__ float s_qc[kAhead][GQ];
@@ -507,11 +506,21 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     prefetch_tmap(&map_v);
   }
   if (warp == 0) {
-    const Line l = walk_line(a, [&](int total) { return share_of(total, a.ctas, blockIdx.x).lo; });
+    Share share;
+    const Line l = walk_line(a, [&](int total) {
+      share = share_of(total, a.ctas, blockIdx.x);
+      return share.lo;
+    });
     if (lane == 0) {
-      s_total = l.total;
-      s_before = l.before;
-      s_b = l.b;
+      s_share = share;
+      if (share.lo < share.hi) {
+        Walk w;
+        w.b = l.b;
+        w.load(a);
+        w.h = (share.lo - l.before) / w.nt;
+        w.t = share.lo - l.before - w.h * w.nt;
+        s_walk = w;
+      }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end itself
@@ -519,8 +528,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Share sh = share_of(s_total, a.ctas, blockIdx.x);
-  const int n = sh.hi - sh.lo;
+  const int n = s_share.hi - s_share.lo;
   // A wait that runs out sets s_abort, after which no wait waits: the TMA and MMA
   // warps stop, the others run through their loops and meet every barrier.
   volatile int* abort = &s_abort;
@@ -531,8 +539,56 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     *abort = 1;
     return false;
   };
+  const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
+  // By one warp: query head g's pieces into buffer qb, K-major rows piece * GQ + g, zero past head_dim and past the
+  // group, and the factor of its logits.  A lane has four columns of every 128.
+  auto query = [&](int64_t unit, int g, int qb) {
+    float v[HDA][4];
+    uint32_t big = 0;
+#pragma unroll
+    for (int x = 0; x < HDA; ++x) {
+      const int j = 128 * x + 4 * lane;
+      typename Pieces<T>::raw raw{};
+      if (g < a.gq && j < a.hd)
+        raw = __ldg(reinterpret_cast<const typename Pieces<T>::raw*>(static_cast<const T*>(a.q) +
+                                                                     (unit * a.gq + g) * a.hd + j));
+      Pieces<T>::open(raw, v[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < HDA; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = __float_as_uint(v[x][e]) & 0x7FFFFFFFu;
+        const bool finite = m < 0x7F800000u;
+        big = max(big, finite ? m : 0u);
+        v[x][e] = finite ? v[x][e] : __uint_as_float(0x7FC00000u);  // makes the head's logits NaN
+      }
+    const int e2 = scale_exp(__reduce_max_sync(0xffffffffu, big));
+    const float inv = pow2f(-e2);
+#pragma unroll
+    for (int x = 0; x < HDA; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[x][e] *= inv;
+#pragma unroll
+    for (int p = 0; p < kNq; ++p)
+#pragma unroll
+      for (int x = 0; x < HDA; ++x) {
+        float* r = v[x];
+        const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
+        *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g, 4 * lane)) =
+            c0 | static_cast<uint32_t>(c1) << 16;
+        if (p + 1 < kNq) {
+          const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
+          r[0] = 16.f * (r[0] - f0.x);
+          r[1] = 16.f * (r[1] - f0.y);
+          r[2] = 16.f * (r[2] - f1.x);
+          r[3] = 16.f * (r[3] - f1.y);
+        }
+      }
+    if (lane == 0) s_qc[qb][g] = pow2f(e2) * q_scale;
+  };
   if (n > 0) {
-    Walk w(a, s_b, sh.lo - s_before);
+    Walk w = s_walk;
     if (warp == kWarpTma) {
       if (lane == 0) {
         int i = 0;
@@ -630,89 +686,31 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       if (elect_one()) umma_commit(&done[1]);
       (void)mbar_wait(&done[1], 0, a.status);
     } else if (warp == kWarpQ) {
-      // queries of one unit: pieces, K-major rows piece * GQ + g, zero past head_dim and past the group
+      // the queries of every unit after the first, as far ahead as there are buffers
       int seg = 0;
-      const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
-      for (int i = 0; i < n;) {
-        const int qb = seg % kAhead;
-        if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
-        const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
-        // a lane has four columns of every 128; eight heads' loads are in flight at a time
-        constexpr int kBatch = GQ < 8 ? GQ : 8;
-#pragma unroll
-        for (int g0 = 0; g0 < GQ; g0 += kBatch) {
-          typename Pieces<T>::raw raw[kBatch][HDA];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int x = 0; x < HDA; ++x) {
-              const int j = 128 * x + 4 * lane;
-              raw[k][x] = typename Pieces<T>::raw{};
-              if (g0 + k < a.gq && j < a.hd)
-                raw[k][x] = *reinterpret_cast<const typename Pieces<T>::raw*>(
-                    static_cast<const T*>(a.q) + (unit * a.gq + g0 + k) * a.hd + j);
-            }
-          // step by step over the batch, so that no step waits for one head's chain
-          float v[kBatch][HDA][4];
-          uint32_t big[kBatch];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            big[k] = 0;
-#pragma unroll
-            for (int x = 0; x < HDA; ++x) {
-              Pieces<T>::open(raw[k][x], v[k][x]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t m = __float_as_uint(v[k][x][e]) & 0x7FFFFFFFu;
-                const bool finite = m < 0x7F800000u;
-                big[k] = max(big[k], finite ? m : 0u);
-                v[k][x][e] = finite ? v[k][x][e] : __uint_as_float(0x7FC00000u);  // makes the head's logits NaN
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) big[k] = __reduce_max_sync(0xffffffffu, big[k]);
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int e2 = scale_exp(big[k]);
-            const float inv = pow2f(-e2);
-#pragma unroll
-            for (int x = 0; x < HDA; ++x)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[k][x][e] *= inv;
-            if (lane == 0) s_qc[qb][g0 + k] = pow2f(e2) * q_scale;
-          }
-#pragma unroll
-          for (int p = 0; p < kNq; ++p)
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-              for (int x = 0; x < HDA; ++x) {
-                float* r = v[k][x];
-                const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
-                *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g0 + k, 4 * lane)) =
-                    c0 | static_cast<uint32_t>(c1) << 16;
-                if (p + 1 < kNq) {
-                  const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
-                  r[0] = 16.f * (r[0] - f0.x);
-                  r[1] = 16.f * (r[1] - f0.y);
-                  r[2] = 16.f * (r[2] - f1.x);
-                  r[3] = 16.f * (r[3] - f1.y);
-                }
-              }
+      for (int i = 0; i < n; ++seg) {
+        if (seg > 0) {
+          const int qb = seg % kAhead;
+          if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
+#pragma unroll 8
+          for (int g = 0; g < GQ; ++g) query(w.b * a.Hkv + w.h, g, qb);
+          fence_proxy_async();
+          mbar_arrive(&q_full[qb]);
         }
-        fence_proxy_async();
-        mbar_arrive(&q_full[qb]);
-        ++seg;
         // to the next unit
-        const int left = w.nt - w.t;
-        i += left;
+        i += w.nt - w.t;
         if (i < n) {
           w.t = w.nt - 1;
           w.step(a);
         }
       }
     } else {
+      // the first unit's queries, which everything waits for, by all softmax warps
+#pragma unroll 1
+      for (int g = warp; g < GQ; g += 8) query(w.b * a.Hkv + w.h, g, 0);
+      fence_proxy_async();
+      named_bar_sync(3, 256);
+      if (warp == 0) mbar_arrive(&q_full[0]);
       const int wg = warp >> 2, row = tid & 127, quarter = warp & 3;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
       const int lb = 31 - __clz(a.block), sub = sub_rows(a.block), ls = min(lb, 5), spt = kTile >> ls;
@@ -756,14 +754,14 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
         const int t0 = w.t, i1 = min(n, i0 + w.nt - t0);
         const int first = i0 + ((i0 ^ wg) & 1);
-        const int len = static_cast<int>(w.len);
+        const int len = w.len;
         const float* ksp = a.k_scale + unit * nblk;
         const float* vsp = a.v_scale + unit * nblk;
         float* wp = a.wpart ? a.wpart + unit * a.tiles_cap * spt * a.gq : nullptr;
         float* wr = a.wref + unit * a.tiles_cap * a.gq;
         int at = (t0 + first - i0) * kTile + row;
         // scales of the warpgroup's tiles, loaded two of them ahead
-        float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f;
+        float ks = 1.f, vs = 1.f, ks1 = 1.f, vs1 = 1.f;  // 1 for rows past the end
         auto scales = [&](int k, float* x, float* y) {
           const int r = at + k * 2 * kTile;
           if (first + 2 * k < i1 && r < len) {
@@ -789,7 +787,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           const bool live = at < len;
           (void)wait(&s_full[sb], (i / kAhead) & 1);
           tc_fence_after();
-          float ks2 = 0.f, vs2 = 0.f;
+          float ks2 = 1.f, vs2 = 1.f;
           if (i + 4 < i1 && at + 4 * kTile < len) {
             ks2 = __ldg(ksp + ((at + 4 * kTile) >> lb));
             vs2 = __ldg(vsp + ((at + 4 * kTile) >> lb));
@@ -814,10 +812,11 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           // O: references are whole numbers, so that every change of one is an exact power of two.
           const uint32_t vb = __float_as_uint(vs), frac = vb & 0x7FFFFFu;  // vs = vm 2^ev, vm in (1/2, 1]
           const float ev = static_cast<float>(static_cast<int>(vb >> 23) - 127 + (frac ? 1 : 0));
-          const float vm = live ? __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kDigitOne : 0.f;
+          const float vm = __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kDigitOne;
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
-            const float x = live ? s[g] * (c[g] * ks) : -INFINITY;
+            s[g] = live ? s[g] : -INFINITY;  // times a positive factor
+            const float x = s[g] * (c[g] * ks);
             const float x0 = redux_max(x), x1 = redux_max(x + ev);
             if (lane == 0) {
               s_max[wg][par][2 * g][quarter] = x0;
@@ -844,10 +843,10 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           for (int g = 0; g < GQ; ++g) {
             const float4 r = ref[g];
             const float ck = c[g] * ks;
-            p[g] = live ? ex2(fmaf(s[g], ck, -r.x)) : 0.f;
+            p[g] = ex2(fmaf(s[g], ck, -r.x));
             l[g] = fmaf(l[g], r.z, p[g]);
             // a NaN is 0 here, and the sum l has it; 1 itself is the largest number below it
-            fix[g] = __float2uint_rn(live ? ex2(fmaf(s[g], ck, ev - r.y)) * vm : 0.f);
+            fix[g] = __float2uint_rn(ex2(fmaf(s[g], ck, ev - r.y)) * vm);
             if (kDigits < 8) fix[g] = min(fix[g], (1u << (4 * (kDigits & 7))) - 1u);
           }
 #pragma unroll
@@ -902,6 +901,12 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           });
           if (row < a.gq) slot[row] = m;
         }
+        if (first >= i1 && row < a.gq) {  // no tile of the unit: a slot that weighs nothing
+          float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * slot_floats(a.gq, a.hd) + a.gq * a.hd + row;
+          slot[0] = -INFINITY;
+#pragma unroll
+          for (int k = 1; k < 5; ++k) slot[k * a.gq] = 0.f;
+        }
         // to the next unit
         i0 = i1;
         if (i0 < n) {
@@ -924,7 +929,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 // units enough, and the launch is a programmatic one: its CTAs find their unit
 // while the attention still runs.
 constexpr int kCombineThreads = 256;
-constexpr int kMaxSlots = 2 * 256;  // of one unit: two for each CTA
+constexpr int kMaxSlots = 2 * 256;      // of one unit: two for each CTA
+constexpr int kWeightBlocks = 64;       // blocks whose weights a CTA has in hand at a time
 
 __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const AttendArgs a, int heads, int head_ctas) {
   __shared__ int s_before, s_total;
@@ -940,11 +946,11 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
       s_total = l.total;
     }
   }
-  const int64_t len = checked_len(a.lens[b], a.capacity, nullptr);
-  const int nt = static_cast<int>((len + kTile - 1) / kTile);
+  const int len = static_cast<int>(checked_len(a.lens[b], a.capacity, a.status));
+  const int nt = (len + kTile - 1) / kTile;
   __syncthreads();
-  const int x0 = s_before + h * nt, x1 = x0 + nt, total = s_total;
-  const int c0 = nt ? cta_of(total, a.ctas, x0) : 0, c1 = nt ? cta_of(total, a.ctas, x1 - 1) : 0;
+  const int x0 = s_before + h * nt;
+  const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x0 + nt - 1) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's partials from here on
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
@@ -952,29 +958,22 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
       for (int i = tid; i < gq * hd; i += kCombineThreads) out[i] = 0.f;
     return;
   }
-  // the slots of the unit: each CTA whose share meets it left one for each
-  // warpgroup that had a tile of it
+  // the unit's slots: two for each CTA whose share meets it
   const int sf = slot_floats(gq, hd), slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
-  auto written = [&](int k) {
-    const Share sh = share_of(total, a.ctas, c0 + k / 2);
-    const int lo = max(sh.lo, x0), hi = min(sh.hi, x1);
-    return k < slots && (hi - lo >= 2 || ((lo - sh.lo) & 1) == (k & 1));
-  };
   // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M)
   auto head = [&](int g, float* f) {
     constexpr int kHeld = 2;  // slots a lane holds: 64 in all, the rest in further rounds
+    const float* s = base + gq * hd + g;
     float M = -INFINITY, L = 0.f;
     for (int from = 0; from < slots; from += 32 * kHeld) {
       float m[kHeld], l[kHeld];
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) {
         const int k = from + 32 * e + lane;
-        const float* s = base + static_cast<int64_t>(k) * sf + gq * hd + g;
-        const bool w = written(k);
-        m[e] = w ? s[0] : -INFINITY;
-        l[e] = w ? (s[gq] + s[2 * gq]) + (s[3 * gq] + s[4 * gq]) : 0.f;
-        if (f && k < slots) f[k] = m[e];
+        const float* x = s + static_cast<int64_t>(k) * sf;
+        m[e] = k < slots ? x[0] : -INFINITY;
+        l[e] = k < slots ? (x[gq] + x[2 * gq]) + (x[3 * gq] + x[4 * gq]) : 0.f;
       }
       float top = M;
 #pragma unroll
@@ -983,12 +982,17 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
       if (top != M) L *= exp2f(M - top);
       M = top;
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e)
-        if (l[e] != 0.f) L += l[e] * (m[e] == M ? 1.f : exp2f(m[e] - M));  // all NaN: m = M = -inf
+      for (int e = 0; e < kHeld; ++e) {
+        // a slot without rows has l = 0; m = M = -inf where all of a unit's logits are NaN
+        const float w = l[e] == 0.f ? 0.f : m[e] == M ? 1.f : exp2f(m[e] - M);
+        if (w != 0.f) L += l[e] * w;
+        const int k = from + 32 * e + lane;
+        if (f && k < slots) f[k] = slots <= 32 * kHeld ? w : l[e] == 0.f ? NAN : m[e];
+      }
     }
+    if (f && slots > 32 * kHeld)  // M has moved since: from the references again
+      for (int k = lane; k < slots; k += 32) f[k] = isnan(f[k]) ? 0.f : f[k] == M ? 1.f : exp2f(f[k] - M);
     L = warp_sum(L);
-    if (f)
-      for (int k = lane; k < slots; k += 32) f[k] = !written(k) ? 0.f : f[k] == M ? 1.f : exp2f(f[k] - M);
     if (lane == 0) {
       s_m[g] = M;
       s_r[g] = 1.f / L;
@@ -1010,7 +1014,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = e * 32 + lane;
-          // an unwritten slot holds anything
+          // a slot without rows holds anything
           const float2 v = f != 0.f && col < pairs ? s[col] : make_float2(0.f, 0.f);
           acc[e].x = fmaf(f, v.x, acc[e].x);
           acc[e].y = fmaf(f, v.y, acc[e].y);
@@ -1032,29 +1036,33 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   }
   for (int g = warp; g < gq; g += 8) head(g, nullptr);
   __syncthreads();
-  const int64_t nblk = a.capacity / a.block;
-  const int n = static_cast<int>((len + a.block - 1) / a.block);
-  const int sub = sub_rows(a.block), spb = a.block / sub, spt = kTile / sub;
-  const int share = gridDim.y - head_ctas;
-  for (int k = (blockIdx.y - head_ctas) * kCombineThreads + tid; k < n; k += share * kCombineThreads) {
-    const int64_t s0 = static_cast<int64_t>(k) * spb, tile = s0 / spt;
-    const float* ref = a.wref + (static_cast<int64_t>(unit) * a.tiles_cap + tile) * gq;
-    const float* p = a.wpart + (static_cast<int64_t>(unit) * a.tiles_cap * spt + s0) * gq;
-    float w = a.weight[unit * nblk + k], sum = 0.f;
-    for (int g0 = 0; g0 < gq; g0 += 4) {
-      float r[4], v[4][4];
+  // sixteen threads (heads) to a block, four blocks a thread
+  const int nblk = static_cast<int>(a.capacity / a.block), n = (len + a.block - 1) / a.block;
+  const int sub = sub_rows(a.block), spb = a.block / sub, per_tile = kTile / a.block;
+  const int g = tid & 15;
+  const float mg = g < gq ? s_m[g] : 0.f, rg = g < gq ? s_r[g] : 0.f;
+  const float* ref = a.wref + static_cast<int64_t>(unit) * a.tiles_cap * gq + g;
+  const float* p = a.wpart + static_cast<int64_t>(unit) * a.tiles_cap * (kTile / sub) * gq + g;
+  float* weight = a.weight + static_cast<int64_t>(unit) * nblk;
+  for (int k0 = (blockIdx.y - head_ctas) * kWeightBlocks; k0 < n; k0 += (gridDim.y - head_ctas) * kWeightBlocks) {
+    float r[4], v[4][4], old[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const bool in = g0 + g < gq;
-        r[g] = in ? ref[g0 + g] - s_m[g0 + g] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + 16 * j + (tid >> 4);
+      const bool in = g < gq && k < n;
+      r[j] = in ? ref[static_cast<int64_t>(k / per_tile) * gq] : 0.f;
+      old[j] = k < n ? weight[k] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[g][e] = in && e < spb ? p[e * gq + g0 + g] : 0.f;
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if (g0 + g < gq) sum = fmaf((v[g][0] + v[g][1]) + (v[g][2] + v[g][3]), exp2f(r[g]) * s_r[g0 + g], sum);
+      for (int e = 0; e < 4; ++e) v[j][e] = in && e < spb ? p[(static_cast<int64_t>(k) * spb + e) * gq] : 0.f;
     }
-    a.weight[unit * nblk + k] = w + sum;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + 16 * j + (tid >> 4);
+      float w = g < gq && k < n ? ((v[j][0] + v[j][1]) + (v[j][2] + v[j][3])) * (exp2f(r[j] - mg) * rg) : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      if (g == 0 && k < n) weight[k] = old[j] + w;
+    }
   }
 }
 
@@ -1404,7 +1412,7 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   int wy = 0;
   if (accumulate) {
     const int64_t nblk = p->capacity / p->block;
-    wy = static_cast<int>(std::min<int64_t>((nblk + kCombineThreads - 1) / kCombineThreads, 64));
+    wy = static_cast<int>(std::min<int64_t>((nblk + kWeightBlocks - 1) / kWeightBlocks, 64));
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units), head_ctas + wy);
