@@ -542,18 +542,21 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
   // By one warp: query head g's pieces into buffer qb, K-major rows piece * GQ + g, zero past head_dim and past the
   // group, and the factor of its logits.  A lane has four columns of every 128.
-  auto query = [&](int64_t unit, int g, int qb) {
-    float v[HDA][4];
-    uint32_t big = 0;
+  using QRaw = typename Pieces<T>::raw;
+  auto query_load = [&](int64_t unit, int g, QRaw* raw) {
 #pragma unroll
     for (int x = 0; x < HDA; ++x) {
       const int j = 128 * x + 4 * lane;
-      typename Pieces<T>::raw raw{};
+      raw[x] = QRaw{};
       if (g < a.gq && j < a.hd)
-        raw = __ldg(reinterpret_cast<const typename Pieces<T>::raw*>(static_cast<const T*>(a.q) +
-                                                                     (unit * a.gq + g) * a.hd + j));
-      Pieces<T>::open(raw, v[x]);
+        raw[x] = __ldg(reinterpret_cast<const QRaw*>(static_cast<const T*>(a.q) + (unit * a.gq + g) * a.hd + j));
     }
+  };
+  auto query_store = [&](const QRaw* raw, int g, int qb) {
+    float v[HDA][4];
+    uint32_t big = 0;
+#pragma unroll
+    for (int x = 0; x < HDA; ++x) Pieces<T>::open(raw[x], v[x]);
 #pragma unroll
     for (int x = 0; x < HDA; ++x)
 #pragma unroll
@@ -686,14 +689,23 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       if (elect_one()) umma_commit(&done[1]);
       (void)mbar_wait(&done[1], 0, a.status);
     } else if (warp == kWarpQ) {
-      // the queries of every unit after the first, as far ahead as there are buffers
+      // the queries of every unit after the first, as far ahead as there are buffers, kBatch heads loaded at a time
+      constexpr int kBatch = GQ < 8 ? GQ : 8;
+      QRaw raw[kBatch][HDA];
       int seg = 0;
       for (int i = 0; i < n; ++seg) {
         if (seg > 0) {
           const int qb = seg % kAhead;
           if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
-#pragma unroll 8
-          for (int g = 0; g < GQ; ++g) query(w.b * a.Hkv + w.h, g, qb);
+          const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+#pragma unroll 1
+          for (int g0 = 0; g0 < GQ; g0 += kBatch) {
+            if (g0 > 0)
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) query_load(unit, g0 + k, raw[k]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) query_store(raw[k], g0 + k, qb);
+          }
           fence_proxy_async();
           mbar_arrive(&q_full[qb]);
         }
@@ -702,12 +714,20 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         if (i < n) {
           w.t = w.nt - 1;
           w.step(a);
+          // in flight while the buffer is waited for
+          const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) query_load(unit, k, raw[k]);
         }
       }
     } else {
       // the first unit's queries, which everything waits for, by all softmax warps
 #pragma unroll 1
-      for (int g = warp; g < GQ; g += 8) query(w.b * a.Hkv + w.h, g, 0);
+      for (int g = warp; g < GQ; g += 8) {
+        QRaw raw[HDA];
+        query_load(static_cast<int64_t>(w.b) * a.Hkv + w.h, g, raw);
+        query_store(raw, g, 0);
+      }
       fence_proxy_async();
       named_bar_sync(3, 256);
       if (warp == 0) mbar_arrive(&q_full[0]);
@@ -1082,10 +1102,6 @@ constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit
 constexpr int kEvictThreads = 256;
 constexpr int64_t kEvictMaxBlocks = 131072;  // three bit-mask arrays of a unit's blocks in shared memory
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Order of a weight among the evictable blocks as an unsigned number: NaN below
 // every number, -0 as 0, and below the protected blocks' 0xFFFFFFFF.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -1094,13 +1110,14 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sums of n small counts f(i) into out[], by the whole CTA.
+// Exclusive prefix sums of n small counts f(i) into out[], by one warp; returns
+// their total.
 template <typename F>
-__device__ inline int block_scan(int n, int* out, int* s_warp, F f) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ inline int warp_scan(int n, int* out, F f) {
+  const int lane = threadIdx.x & 31;
   int carry = 0;
-  for (int base = 0; base < n; base += kEvictThreads) {
-    const int i = base + tid;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
     const int v = i < n ? f(i) : 0;
     int inc = v;
 #pragma unroll
@@ -1108,15 +1125,8 @@ __device__ inline int block_scan(int n, int* out, int* s_warp, F f) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    int add = carry;
-    for (int w = 0; w < kEvictThreads / 32; ++w) {
-      if (w < warp) add += s_warp[w];
-      carry += s_warp[w];
-    }
-    if (i < n) out[i] = add + inc - v;
-    __syncthreads();
+    if (i < n) out[i] = carry + inc - v;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
   }
   return carry;
 }
@@ -1139,16 +1149,16 @@ __device__ __forceinline__ int find_word(const int* pref, int lo, int hi, int r)
 }
 
 // One cluster per unit.  Every CTA selects the `budget` blocks with the largest
-// keys itself (radix selection, eight bits a pass, on up to 131072 keys), then
-// the warps of the cluster move the kept blocks that stand past the budget into
-// the slots set free below it.  Slots read (>= budget - 1) and written (< budget)
-// meet only in slot budget - 1, which the last move writes behind a barrier.
+// keys itself (radix selection, eight bits a pass; up to 2048 keys stay in
+// registers), then the warps of the cluster move the kept blocks that stand past
+// the budget into the slots set free below it.  Slots read (>= budget - 1) and
+// written (< budget) meet only in slot budget - 1, which the last move writes:
+// the warp that moves a piece out of it moves the last block's piece in.
 __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_dyn[];
-  __shared__ uint32_t s_hist[256];
-  __shared__ int s_warp[kEvictThreads / 32];
+  __shared__ uint32_t s_hist[2][256];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_need, s_moves;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % kEvictCtas, unit = blockIdx.x / kEvictCtas, b = unit / a.Hkv;
   const int64_t len = checked_len(a.lens[b], a.capacity, a.status);
@@ -1161,32 +1171,61 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   const int64_t nblk = a.capacity / a.block;
   const float* weight = a.weight + unit * nblk;
   const int32_t* ids = a.ids + unit * nblk;
+  constexpr int kHeld = 8;  // keys a thread holds
+  const bool held = n <= kHeld * kEvictThreads;
   const int last = ids[n - 1];
-  auto key = [&](int i) {
-    const int id = ids[i];
+  auto key_of = [&](int i, float w, int id) {
     const bool safe = id < a.sink || static_cast<int64_t>(id) > static_cast<int64_t>(last) - a.recent || i == n - 1;
-    return safe ? 0xFFFFFFFFu : weight_key(weight[i]);
+    return safe ? 0xFFFFFFFFu : weight_key(w);
+  };
+  uint32_t mine[kHeld];
+  if (held) {
+    float w[kHeld];
+    int id[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = tid + k * kEvictThreads;
+      w[k] = i < n ? weight[i] : 0.f;
+      id[k] = i < n ? ids[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) mine[k] = key_of(tid + k * kEvictThreads, w[k], id[k]);
+  }
+  // f(i, key) for the thread's slots, a warp's together
+  auto each = [&](auto f) {
+    if (held) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (k * kEvictThreads < n) f(tid + k * kEvictThreads, mine[k]);
+    } else {
+      for (int base = 0; base < n; base += kEvictThreads) {
+        const int i = base + tid;
+        f(i, i < n ? key_of(i, weight[i], ids[i]) : 0u);
+      }
+    }
   };
   // the budget-th largest key
   if (tid == 0) {
     s_prefix = 0;
     s_need = a.budget;
   }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[tid] = 0;
+  s_hist[0][tid] = 0;
+  __syncthreads();
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    uint32_t* hist = s_hist[pass & 1];
+    const uint32_t prefix = s_prefix, mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    each([&](int i, uint32_t u) {
+      if (i < n && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+    });
     __syncthreads();
-    const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = tid; i < n; i += kEvictThreads) {
-      const uint32_t u = key(i);
-      if ((u & mask) == prefix) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
-    }
-    __syncthreads();
+    s_hist[~pass & 1][tid] = 0;
     if (warp == 0) {
       // lane l holds bins 255 - 8 l .. 248 - 8 l; the first bin, from above, that reaches the need
       uint32_t c[8], sum = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        c[k] = s_hist[255 - 8 * lane - k];
+        c[k] = hist[255 - 8 * lane - k];
         sum += c[k];
       }
       uint32_t inc = sum;
@@ -1197,6 +1236,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
       }
       const uint32_t need = static_cast<uint32_t>(s_need);
       uint32_t above = inc - sum;
+      __syncwarp();
       if (above < need && inc >= need) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -1217,23 +1257,23 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   const int need = s_need;
   const int nw = (n + 31) / 32;
   uint32_t* keep = s_dyn;
-  int* pref_a = reinterpret_cast<int*>(s_dyn + nw);
+  int* pref_m = reinterpret_cast<int*>(s_dyn + nw);
   uint32_t* equal = s_dyn + 2 * nw;
-  for (int w = warp; w < nw; w += kEvictThreads / 32) {
-    const int i = w * 32 + lane;
-    const uint32_t u = i < n ? key(i) : 0u;
+  each([&](int i, uint32_t u) {
     const unsigned gt = __ballot_sync(0xffffffffu, i < n && u > threshold);
     const unsigned eq = __ballot_sync(0xffffffffu, i < n && u == threshold);
-    if (lane == 0) {
-      keep[w] = gt;
-      equal[w] = eq;
+    if (lane == 0 && i < n) {
+      keep[i >> 5] = gt;
+      equal[i >> 5] = eq;
     }
-  }
+  });
+  // this CTA has read weights and numbers: others may change them once all have
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   __syncthreads();
-  cluster_sync();  // every CTA of the unit has read its keys: the arrays may change from here
-  block_scan(nw, pref_a, s_warp, [&](int w) { return __popc(equal[w]); });
+  if (warp == 0) warp_scan(nw, pref_m, [&](int w) { return __popc(equal[w]); });
+  __syncthreads();
   for (int w = tid; w < nw; w += kEvictThreads) {
-    int take = need - pref_a[w];
+    int take = need - pref_m[w];
     uint32_t eq = equal[w], add = 0;
     while (take > 0 && eq) {
       add |= eq & (0u - eq);
@@ -1248,38 +1288,68 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   const uint32_t below = (1u << (edge & 31)) - 1u;
   auto mover = [&](int w) { return w < we ? 0u : w == we ? keep[w] & ~below : keep[w]; };
   auto empty = [&](int w) { return w < we ? ~keep[w] : (~keep[w] & below) | (1u << (edge & 31)); };
-  int* pref_m = pref_a;
   int* pref_f = reinterpret_cast<int*>(equal);
-  const int moves = block_scan(nw, pref_m, s_warp, [&](int w) { return __popc(mover(w)); });
-  block_scan(we + 1, pref_f, s_warp, [&](int w) { return __popc(empty(w)); });
-  // The moves' bytes in pieces of 32 x 8 vectors, dealt out to the cluster's warps: a warp has a piece's
-  // loads in flight together.
-  const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
-  auto move = [&](int r, int x, int piece) __attribute__((always_inline)) {
+  if (warp == 0) {
+    const int moves = warp_scan(nw, pref_m, [&](int w) { return __popc(mover(w)); });
+    if (lane == 0) s_moves = moves;
+  } else if (warp == 1) {
+    warp_scan(we + 1, pref_f, [&](int w) { return __popc(empty(w)); });
+  }
+  __syncthreads();
+  // Moves r = 0 .. moves - 1, the last one (slot n - 1 to slot budget - 1) together with the first.
+  const int moves = s_moves, rounds = max(moves - 1, 1);
+  const bool pair = moves > 1;
+  auto place = [&](int r, int* src, int* dst) {
     const int wm = find_word(pref_m, 0, nw, r), wf = find_word(pref_f, 0, we + 1, r);
-    const int64_t src = wm * 32 + nth_bit(mover(wm), r - pref_m[wm]);
-    const int64_t dst = wf * 32 + nth_bit(empty(wf), r - pref_f[wf]);
-    const uint4* from = reinterpret_cast<const uint4*>(a.code[x] + (unit * a.capacity + src * a.block) * a.hd);
-    uint4* to = reinterpret_cast<uint4*>(a.code[x] + (unit * a.capacity + dst * a.block) * a.hd);
-    uint4 v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (piece * 256 + k * 32 + lane < nv) v[k] = from[piece * 256 + k * 32 + lane];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (piece * 256 + k * 32 + lane < nv) to[piece * 256 + k * 32 + lane] = v[k];
-    if (piece == 0 && lane == 0) {
-      const int64_t o = unit * nblk;
-      a.scale[x][o + dst] = a.scale[x][o + src];
-      if (x == 0) a.weight[o + dst] = a.weight[o + src];
-      else a.ids[o + dst] = a.ids[o + src];
-    }
+    *src = wm * 32 + nth_bit(mover(wm), r - pref_m[wm]);
+    *dst = wf * 32 + nth_bit(empty(wf), r - pref_f[wf]);
   };
+  // the codes in pieces of 32 x 8 vectors, dealt out to the cluster's warps, a piece's loads in flight together
   constexpr int kWarps = kEvictCtas * kEvictThreads / 32;
-  for (int64_t w = warp * kEvictCtas + rank; w < static_cast<int64_t>(moves - 1) * 2 * per; w += kWarps)
-    move(static_cast<int>(w / (2 * per)), static_cast<int>(w / per) & 1, static_cast<int>(w % per));
-  cluster_sync();  // slot budget - 1 has been read
-  for (int w = warp * kEvictCtas + rank; w < 2 * per; w += kWarps) move(moves - 1, w / per, w % per);
+  const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
+  const int me = warp * kEvictCtas + rank;
+  for (int64_t w = me; w < static_cast<int64_t>(rounds) * 2 * per; w += kWarps) {
+    const int r = static_cast<int>(w / (2 * per)), q = static_cast<int>(w - static_cast<int64_t>(r) * 2 * per);
+    const int x = q >= per, first = (x ? q - per : q) * 256 + lane;
+    int src, dst;
+    place(r, &src, &dst);
+    uint4* rows = reinterpret_cast<uint4*>((x ? a.code[1] : a.code[0]) + unit * a.capacity * a.hd) + first;
+    uint4 v[8], z[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + 32 * k < nv) v[k] = rows[static_cast<int64_t>(src) * nv + 32 * k];
+    if (r == 0 && pair) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (first + 32 * k < nv) z[k] = rows[static_cast<int64_t>(n - 1) * nv + 32 * k];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + 32 * k] = v[k];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (first + 32 * k < nv) rows[static_cast<int64_t>(edge) * nv + 32 * k] = z[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + 32 * k] = v[k];
+    }
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // scales, weights and numbers: lane l < 4 has one of the four arrays
+  for (int r = me; r < rounds; r += kWarps) {
+    int src, dst;
+    place(r, &src, &dst);
+    if (lane < 4) {
+      uint32_t* x = lane == 0   ? reinterpret_cast<uint32_t*>(a.scale[0])
+                    : lane == 1 ? reinterpret_cast<uint32_t*>(a.scale[1])
+                    : lane == 2 ? reinterpret_cast<uint32_t*>(a.weight)
+                                : reinterpret_cast<uint32_t*>(a.ids);
+      x += unit * nblk;
+      const uint32_t v = x[src], z = x[n - 1];
+      x[dst] = v;
+      if (r == 0 && pair) x[edge] = z;
+    }
+  }
   if (writes_len) a.lens_out[b] = static_cast<int32_t>(len - static_cast<int64_t>(n - a.budget) * a.block);
 }
 
