@@ -478,7 +478,8 @@ class KV8Cache:
             if t is not None and t.shape != k_scale.shape:
                 raise ValueError("scales, weight and ids need one shape")
         self.k, self.v, self.k_scale, self.v_scale, self.weight, self.ids = k, v, k_scale, v_scale, weight, ids
-        self.device = k.device
+        self.index = k.get_device()
+        self.sizes = (*k.shape, k.shape[2] // k_scale.shape[2])
         self.pointers = KV8Pointers(*(_ptr(t) for t in (k, v, k_scale, v_scale, weight, ids)))
 
     @classmethod
@@ -493,16 +494,15 @@ class KV8Cache:
                    torch.empty(nblk, dtype=torch.int32, device=device))
 
 
-def _kv8_check(p: KV8Params, cache: KV8Cache, lens, *tensors):
-    """Shapes that the C call cannot see: the cache is p's, lens and the other [B] arrays are
-    int32, and everything lies on the current device."""
-    if tuple(cache.k.shape) != (p.batch, p.n_kv_heads, p.capacity, p.head_dim) or \
-            cache.k_scale.shape[2] * p.block != p.capacity:
+def _kv8_check(p: KV8Params, cache: KV8Cache, *tensors):
+    """What the C call cannot see: the cache is p's and everything lies on the current device."""
+    if cache.sizes != (p.batch, p.n_kv_heads, p.capacity, p.head_dim, p.block):
         raise ValueError("the cache's tensors do not have p's sizes")
-    if cache.device.index != torch.cuda.current_device():
+    device = cache.index
+    if device != torch.cuda.current_device():
         raise ValueError("the cache is not on the current CUDA device")
-    for t in (lens, *tensors):
-        if t is not None and t.device != cache.device:
+    for t in tensors:
+        if t is not None and t.get_device() != device:
             raise ValueError("all tensors must be on the cache's device")
 
 
@@ -518,16 +518,17 @@ def xkv_kv8_append(p: KV8Params, cache: KV8Cache, lens, k_new, v_new, counts=Non
     """Round new rows k_new, v_new [B][n][Hkv hd] (views with contiguous rows are accepted) into the
     cache at positions lens[b] ...; counts[b] <= n rows where given.  lens is not advanced."""
     _kv8_check(p, cache, lens, k_new, v_new, counts)
-    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype or \
-            k_new.shape[0] != p.batch or k_new.shape[2] != p.n_kv_heads * p.head_dim:
+    shape, strides, dtype = k_new.shape, k_new.stride(), k_new.dtype
+    if len(shape) != 3 or v_new.shape != shape or v_new.dtype != dtype or shape[0] != p.batch or \
+            shape[2] != p.n_kv_heads * p.head_dim:
         raise ValueError("k_new and v_new are [B][n][Hkv hd] of one dtype")
-    n = k_new.shape[1]
-    if k_new.stride(2) != 1 or (k_new.stride() != v_new.stride()):
+    if strides[2] != 1 or v_new.stride() != strides:
         raise ValueError("k_new and v_new need contiguous rows and the same strides")
-    ld = k_new.stride(1) if n > 1 else max(k_new.stride(1), k_new.shape[2])
-    _check(lib.xkv_kv8_append(p, cache.pointers, _lens_ptr(p, lens), _lens_ptr(p, counts), n,
-                              dtype_code(k_new.dtype), k_new.data_ptr(), v_new.data_ptr(), ld,
-                              k_new.stride(0) if p.batch > 1 else 0, _stream(stream)), "xkv_kv8_append")
+    # a stride over one row or one sequence is not used, and torch leaves it open
+    _check(lib.xkv_kv8_append(p, cache.pointers, _lens_ptr(p, lens), _lens_ptr(p, counts), shape[1],
+                              dtype_code(dtype), k_new.data_ptr(), v_new.data_ptr(),
+                              strides[1] if shape[1] > 1 else shape[2], strides[0] if shape[0] > 1 else 0,
+                              _stream(stream)), "xkv_kv8_append")
 
 
 def xkv_kv8_workspace_size(p: KV8Params, n_q_heads: int) -> int:
@@ -539,10 +540,11 @@ def xkv_kv8_attention_decode(p: KV8Params, cache: KV8Cache, lens, q, out, accumu
     """One decode step over the 8-bit cache; writes out [B][Hq][hd] f32 and, with accumulate, adds
     every block's attention weight to cache.weight."""
     _kv8_check(p, cache, lens, q, out, ws)
-    if q.dim() != 3 or q.shape[0] != p.batch or q.shape[2] != p.head_dim or out.shape != q.shape or \
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != p.batch or shape[2] != p.head_dim or out.shape != shape or \
             out.dtype != torch.float32:
         raise ValueError("q is [B][Hq][hd] and out the same shape in float32")
-    n_q_heads = q.shape[1]
+    n_q_heads = shape[1]
     ws = ws if ws is not None else workspace(xkv_kv8_workspace_size(p, n_q_heads), q.device)
     _check(lib.xkv_kv8_attention_decode(p, cache.pointers, _lens_ptr(p, lens), n_q_heads, dtype_code(q.dtype), _ptr(q),
                                         _ptr(out), int(bool(accumulate)), _ptr(ws), ws.numel() * ws.element_size(),

@@ -211,6 +211,10 @@ __host__ __device__ inline int sub_rows(int block) { return block < 32 ? block :
 
 // Units' tiles stand in one line (sequence, head, tile), and CTA c of n takes a
 // contiguous share of it: ragged lengths need no more CTAs than the card runs.
+// A unit of nt tiles takes nt + 1 places, the last one empty: starting and
+// ending a unit costs a CTA about as much as a tile (2.2 and 4.4 thousand clocks
+// for a tile of a long unit and a unit of one tile, 8 query heads of 64 columns;
+// 48 sequences of 1 to 8192 tokens took 32 us by tiles alone).
 struct Share {
   int lo, hi;
 };
@@ -234,69 +238,81 @@ __device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) { return (rows_of(a, b) + kTile - 1) / kTile; }
 
-// By one warp: the tiles in all, and a place in their line: sequence b and the
-// tiles before it.  `place` turns the total into the tile looked for, or into
-// -1 - b where a sequence b is; the last sequence has no tile behind it and a
-// tile past the end is at b = B.
-struct Line {
-  int before, total, b;
+__device__ __forceinline__ int places_of(int nt) { return nt ? nt + 1 : 0; }
+
+// By one warp: N places of the line.  `targets` turns the line's length into
+// the places looked for, or -1 - b where the start of sequence b is.  A place is
+// told as its sequence b, the places and the units that have rows before b; a
+// place past the end is at b = B.
+struct Spot {
+  int b, before, units;
 };
-template <typename F>
-__device__ inline Line walk_line(const AttendArgs& a, F place) {
+template <int N, typename F>
+__device__ inline int walk_line(const AttendArgs& a, Spot* spot, F targets) {
   constexpr int kEach = 4;  // sequences a lane takes at a time
   const int lane = threadIdx.x & 31;
-  Line r{0, 0, a.B};
-  int n[kEach], at = 0;
-  // tiles of sequences base + kEach lane ..., and those before them from `carry` on
-  auto load = [&](int base, int carry) {
-    int sum = 0;
+  int n[kEach];
+  int64_t at = 0;  // units << 32 | places before the lane's first sequence
+  auto load = [&](int base, int64_t carry) {
+    int64_t sum = 0;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int b = base + lane * kEach + k;
-      n[k] = b < a.B ? tiles_of(a, b) * a.Hkv : 0;
+      n[k] = b < a.B ? places_of(tiles_of(a, b)) * a.Hkv : 0;
+      sum += n[k] ? static_cast<int64_t>(a.Hkv) << 32 | n[k] : 0;
     }
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) sum += n[k];
-    int inc = sum;
+    int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     at = carry + inc - sum;
     return carry + __shfl_sync(0xffffffffu, inc, 31);
   };
-  for (int base = 0; base < a.B; base += 32 * kEach) r.total = load(base, r.total);
-  const int x = place(r.total);
-  for (int base = 0, carry = 0; base < a.B; base += 32 * kEach) {
-    if (a.B > 32 * kEach) carry = load(base, carry);  // else what was loaded still stands
-    int hit_b = -1, hit_at = 0, p = at;
+  int64_t all = 0;
+  for (int base = 0; base < a.B; base += 32 * kEach) all = load(base, all);
+  const int total = static_cast<int>(all);
+  int x[N];
+  targets(total, x);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int b = base + lane * kEach + k;
-      if (x >= 0 ? (x >= p && x < p + n[k]) : b == -1 - x) {
-        hit_b = b;
-        hit_at = p;
+  for (int t = 0; t < N; ++t) spot[t] = Spot{a.B, total, static_cast<int>(all >> 32)};
+  int64_t carry = 0;
+  for (int base = 0; base < a.B; base += 32 * kEach) {
+    if (a.B > 32 * kEach) carry = load(base, carry);  // else what was loaded still stands
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      int hit_b = -1;
+      int64_t hit_at = 0, p = at;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int b = base + lane * kEach + k, q = static_cast<int>(p);
+        if (x[t] >= 0 ? (x[t] >= q && x[t] < q + n[k]) : b == -1 - x[t]) {
+          hit_b = b;
+          hit_at = p;
+        }
+        p += n[k] ? static_cast<int64_t>(a.Hkv) << 32 | n[k] : 0;
       }
-      p += n[k];
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, hit_b >= 0);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.b = __shfl_sync(0xffffffffu, hit_b, src);
-      r.before = __shfl_sync(0xffffffffu, hit_at, src);
-      break;
+      const unsigned hit = __ballot_sync(0xffffffffu, hit_b >= 0);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        spot[t].b = __shfl_sync(0xffffffffu, hit_b, src);
+        const int64_t f = __shfl_sync(0xffffffffu, hit_at, src);
+        spot[t].before = static_cast<int>(f);
+        spot[t].units = static_cast<int>(f >> 32);
+      }
     }
   }
-  return r;
+  return total;
 }
 
 // One role's position in its CTA's share: tile t of the nt tiles of unit (b, h).
 struct Walk {
-  int b, h, t, nt, len;
-  __device__ __forceinline__ void load(const AttendArgs& a) {
-    len = rows_of(a, b);
+  int b, h, t, nt, len, ahead;  // ahead: the next sequence's rows, loaded before they are needed
+  __device__ __forceinline__ void load(const AttendArgs& a, int rows) {
+    len = rows;
     nt = (len + kTile - 1) / kTile;
+    ahead = b + 1 < a.B ? rows_of(a, b + 1) : 0;
   }
   // The next tile; only where there is one.
   __device__ __forceinline__ void step(const AttendArgs& a) {
@@ -306,7 +322,7 @@ struct Walk {
     h = 0;
     do {
       ++b;
-      load(a);
+      load(a, ahead);
     } while (nt == 0);
   }
 };
@@ -467,7 +483,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ __align__(8) uint64_t s_full[kAhead], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ Share s_share;
+  __shared__ int s_tiles;
   __shared__ Walk s_walk;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
@@ -506,21 +522,32 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     prefetch_tmap(&map_v);
   }
   if (warp == 0) {
-    Share share;
-    const Line l = walk_line(a, [&](int total) {
+    Spot spot[2];
+    Share share{0, 0};
+    walk_line<2>(a, spot, [&](int total, int* x) {
       share = share_of(total, a.ctas, blockIdx.x);
-      return share.lo;
+      x[0] = share.lo;
+      x[1] = share.hi;
     });
     if (lane == 0) {
-      s_share = share;
+      int n = 0;
       if (share.lo < share.hi) {
         Walk w;
-        w.b = l.b;
-        w.load(a);
-        w.h = (share.lo - l.before) / w.nt;
-        w.t = share.lo - l.before - w.h * w.nt;
+        w.b = spot[0].b;
+        w.load(a, rows_of(a, w.b));
+        w.h = (share.lo - spot[0].before) / (w.nt + 1);
+        w.t = share.lo - spot[0].before - w.h * (w.nt + 1);
+        // the share's tiles: its places less the empty one of every unit that ends in it
+        const int each = spot[1].b < a.B ? places_of(tiles_of(a, spot[1].b)) : 1;
+        n = share.hi - share.lo -
+            (spot[1].units + (share.hi - spot[1].before) / each - (spot[0].units + w.h));
+        if (n > 0 && w.t == w.nt) {  // the share starts with an empty place
+          w.t = w.nt - 1;
+          w.step(a);
+        }
         s_walk = w;
       }
+      s_tiles = n;
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end itself
@@ -528,7 +555,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int n = s_share.hi - s_share.lo;
+  const int n = s_tiles;
   // A wait that runs out sets s_abort, after which no wait waits: the TMA and MMA
   // warps stop, the others run through their loops and meet every barrier.
   volatile int* abort = &s_abort;
@@ -540,25 +567,27 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     return false;
   };
   const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
-  // By one warp: query head g's pieces into buffer qb, K-major rows piece * GQ + g, zero past head_dim and past the
-  // group, and the factor of its logits.  A lane has four columns of every 128.
+  // By one warp, four query heads at a time, eight lanes to a head: their pieces into buffer qb, K-major rows
+  // piece * GQ + g, zero past head_dim and past the group, and the factor of their logits.  A lane has four columns
+  // of every 32; what it does is a chain of short steps, and these run side by side.
   using QRaw = typename Pieces<T>::raw;
-  auto query_load = [&](int64_t unit, int g, QRaw* raw) {
+  constexpr int kQuads = 4 * HDA;
+  const int q_head = lane >> 3, q_col = 4 * (lane & 7);
+  auto query_load = [&](int64_t unit, int g0, QRaw* raw) {
+    const T* q = static_cast<const T*>(a.q) + (unit * a.gq + g0 + q_head) * a.hd;
 #pragma unroll
-    for (int x = 0; x < HDA; ++x) {
-      const int j = 128 * x + 4 * lane;
+    for (int x = 0; x < kQuads; ++x) {
+      const int j = 32 * x + q_col;
       raw[x] = QRaw{};
-      if (g < a.gq && j < a.hd)
-        raw[x] = __ldg(reinterpret_cast<const QRaw*>(static_cast<const T*>(a.q) + (unit * a.gq + g) * a.hd + j));
+      if (g0 + q_head < a.gq && j < a.hd) raw[x] = __ldg(reinterpret_cast<const QRaw*>(q + j));
     }
   };
-  auto query_store = [&](const QRaw* raw, int g, int qb) {
-    float v[HDA][4];
+  auto query_store = [&](const QRaw* raw, int g0, int qb) {
+    float v[kQuads][4];
     uint32_t big = 0;
 #pragma unroll
-    for (int x = 0; x < HDA; ++x) Pieces<T>::open(raw[x], v[x]);
-#pragma unroll
-    for (int x = 0; x < HDA; ++x)
+    for (int x = 0; x < kQuads; ++x) {
+      Pieces<T>::open(raw[x], v[x]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t m = __float_as_uint(v[x][e]) & 0x7FFFFFFFu;
@@ -566,19 +595,24 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         big = max(big, finite ? m : 0u);
         v[x][e] = finite ? v[x][e] : __uint_as_float(0x7FC00000u);  // makes the head's logits NaN
       }
-    const int e2 = scale_exp(__reduce_max_sync(0xffffffffu, big));
-    const float inv = pow2f(-e2);
+    }
 #pragma unroll
-    for (int x = 0; x < HDA; ++x)
+    for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const int e2 = scale_exp(big);
+    const float inv = pow2f(-e2);
+    if ((lane & 7) == 0) s_qc[qb][g0 + q_head] = pow2f(e2) * q_scale;
+#pragma unroll
+    for (int x = 0; x < kQuads; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[x][e] *= inv;
 #pragma unroll
     for (int p = 0; p < kNq; ++p)
 #pragma unroll
-      for (int x = 0; x < HDA; ++x) {
+      for (int x = 0; x < kQuads; ++x) {
         float* r = v[x];
         const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
-        *reinterpret_cast<uint32_t*>(sq + (qb * HDA + x) * Sh::ns * 128 + swz128(p * GQ + g, 4 * lane)) =
+        uint8_t* to = sq + (qb * HDA + x / 4) * Sh::ns * 128;
+        *reinterpret_cast<uint32_t*>(to + swz128(p * GQ + g0 + q_head, 32 * (x % 4) + q_col)) =
             c0 | static_cast<uint32_t>(c1) << 16;
         if (p + 1 < kNq) {
           const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
@@ -588,7 +622,6 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           r[3] = 16.f * (r[3] - f1.y);
         }
       }
-    if (lane == 0) s_qc[qb][g] = pow2f(e2) * q_scale;
   };
   if (n > 0) {
     Walk w = s_walk;
@@ -689,44 +722,50 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       if (elect_one()) umma_commit(&done[1]);
       (void)mbar_wait(&done[1], 0, a.status);
     } else if (warp == kWarpQ) {
-      // the queries of every unit after the first, as far ahead as there are buffers, kBatch heads loaded at a time
-      constexpr int kBatch = GQ < 8 ? GQ : 8;
-      QRaw raw[kBatch][HDA];
-      int seg = 0;
-      for (int i = 0; i < n; ++seg) {
-        if (seg > 0) {
-          const int qb = seg % kAhead;
-          if (seg >= kAhead) (void)wait(&q_empty[qb], ((seg / kAhead) & 1) ^ 1);
-          const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+      // the queries of every unit after the first, as far ahead as there are buffers; the next unit's are loaded
+      // (32 registers of them at most) while one is cut into pieces
+      constexpr int kMost = 128 / (kQuads * static_cast<int>(sizeof(QRaw)));
+      constexpr int kBatch = kMost < GQ / 4 ? kMost : GQ / 4;
+      QRaw raw[kBatch][kQuads], next[kBatch][kQuads];
+      int64_t unit = 0;
+      int seg = -1;
+      for (int i = 0; seg < 0 || unit >= 0; ++seg) {
+        // the unit after this one
+        i += w.nt - w.t;
+        int64_t after = -1;
+        if (i < n) {
+          w.t = w.nt - 1;
+          w.step(a);
+          after = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) query_load(after, 4 * k, next[k]);
+        }
+        if (seg >= 0) {
+          const int s1 = seg + 1, qb = s1 % kAhead;
+          if (s1 >= kAhead) (void)wait(&q_empty[qb], ((s1 / kAhead) & 1) ^ 1);
 #pragma unroll 1
-          for (int g0 = 0; g0 < GQ; g0 += kBatch) {
+          for (int g0 = 0; g0 < GQ; g0 += 4 * kBatch) {
             if (g0 > 0)
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) query_load(unit, g0 + k, raw[k]);
+              for (int k = 0; k < kBatch; ++k) query_load(unit, g0 + 4 * k, raw[k]);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) query_store(raw[k], g0 + k, qb);
+            for (int k = 0; k < kBatch; ++k) query_store(raw[k], g0 + 4 * k, qb);
           }
           fence_proxy_async();
           mbar_arrive(&q_full[qb]);
         }
-        // to the next unit
-        i += w.nt - w.t;
-        if (i < n) {
-          w.t = w.nt - 1;
-          w.step(a);
-          // in flight while the buffer is waited for
-          const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
+        unit = after;
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) query_load(unit, k, raw[k]);
-        }
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+          for (int x = 0; x < kQuads; ++x) raw[k][x] = next[k][x];
       }
     } else {
-      // the first unit's queries, which everything waits for, by all softmax warps
-#pragma unroll 1
-      for (int g = warp; g < GQ; g += 8) {
-        QRaw raw[HDA];
-        query_load(static_cast<int64_t>(w.b) * a.Hkv + w.h, g, raw);
-        query_store(raw, g, 0);
+      // the first unit's queries, which everything waits for, by a softmax warp for every four heads
+      if (warp < GQ / 4) {
+        QRaw raw[kQuads];
+        query_load(static_cast<int64_t>(w.b) * a.Hkv + w.h, 4 * warp, raw);
+        query_store(raw, 4 * warp, 0);
       }
       fence_proxy_async();
       named_bar_sync(3, 256);
@@ -960,16 +999,17 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == 0) {
-    const Line l = walk_line(a, [&](int) { return -1 - b; });
+    Spot spot;
+    const int total = walk_line<1>(a, &spot, [&](int, int* x) { x[0] = -1 - b; });
     if (lane == 0) {
-      s_before = l.before;
-      s_total = l.total;
+      s_before = spot.before;
+      s_total = total;
     }
   }
   const int len = static_cast<int>(checked_len(a.lens[b], a.capacity, a.status));
   const int nt = (len + kTile - 1) / kTile;
   __syncthreads();
-  const int x0 = s_before + h * nt;
+  const int x0 = s_before + h * (nt + 1);
   const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x0 + nt - 1) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's partials from here on
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;

@@ -715,7 +715,7 @@ static xkv_status check_kv8(const xkv_kv8_params* p) {
   if (p->head_dim % 16 != 0 || p->head_dim > 256) return XKV_ERR_UNSUPPORTED;
   if (p->block < 8 || p->block > 128 || (p->block & (p->block - 1)) != 0) return XKV_ERR_UNSUPPORTED;
   const int64_t units = static_cast<int64_t>(p->batch) * p->n_kv_heads, most = int64_t(1) << 30;
-  if (p->capacity > most || units > most || units * ((p->capacity + 127) / 128) > most) return XKV_ERR_UNSUPPORTED;
+  if (p->capacity > most || units > most || units * ((p->capacity + 127) / 128 + 1) > most) return XKV_ERR_UNSUPPORTED;
   return XKV_OK;
 }
 

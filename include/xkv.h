@@ -442,7 +442,7 @@ XKV_API xkv_status xkv_dense_attention_decode(const xkv_dense_params* p, const v
  * [0, capacity] is taken as the nearer end and XKV_ERR_INVALID_ARG is recorded
  * in the device status word.
  * head_dim is a multiple of 16 up to 256; block is 8, 16, 32, 64 or 128 and
- * divides capacity; B Hkv ceil(capacity / 128) <= 2^30 (else
+ * divides capacity; B Hkv (ceil(capacity / 128) + 1) <= 2^30 (else
  * XKV_ERR_UNSUPPORTED).  k and v are 16-byte aligned; the arrays of scales,
  * weights, ids and lengths need only their elements' 4 bytes. */
 typedef struct xkv_kv8_params {
