@@ -47,6 +47,13 @@ __device__ __forceinline__ int64_t checked_len(int32_t n, int64_t most, int* sta
   return n < 0 ? 0 : most;
 }
 
+// Programmatic launches: let the next kernel begin, and wait for the earlier ones.
+// Every block waits, so that a kernel's end stands for the end of all before it.
+// What an earlier kernel may write is read with plain loads, not read-only ones:
+// it can still be running when this kernel starts.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- append
 struct AppendArgs {
   const void* src[2];  // K, V rows
@@ -69,8 +76,8 @@ template <>
 struct Raw16<__nv_bfloat16> {
   uint4 w[2];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    w[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    w[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = reinterpret_cast<const uint4*>(p)[0];
+    w[1] = reinterpret_cast<const uint4*>(p)[1];
   }
   __device__ __forceinline__ float4 quad(int q) const {  // elements 4 q .. 4 q + 3
     const uint4& u = w[q >> 1];
@@ -83,7 +90,7 @@ struct Raw16<float> {
   float4 w[4];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const float4*>(p)[i];
   }
   __device__ __forceinline__ float4 quad(int q) const { return w[q]; }
 };
@@ -103,6 +110,8 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs a) {
   i >>= 1;
   const int j = i % a.nb;
   const int b = i / a.nb;
+  let_next_start();
+  wait_for_earlier();
   const int64_t len = checked_len(a.lens[b], a.capacity, a.status);
   int64_t count = a.counts ? a.counts[b] : a.n_new;
   if (count < 0 || count > a.n_new || len + count > a.capacity) {
@@ -251,56 +260,67 @@ template <int N, typename F>
 __device__ inline int walk_line(const AttendArgs& a, Spot* spot, F targets) {
   constexpr int kEach = 4;  // sequences a lane takes at a time
   const int lane = threadIdx.x & 31;
-  int n[kEach];
-  int64_t at = 0;  // units << 32 | places before the lane's first sequence
-  auto load = [&](int base, int64_t carry) {
-    int64_t sum = 0;
+  int n[kEach], at = 0;  // the lane's sequences' places, and those before them
+  auto load = [&](int base, int carry) {
+    int sum = 0;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int b = base + lane * kEach + k;
       n[k] = b < a.B ? places_of(tiles_of(a, b)) * a.Hkv : 0;
-      sum += n[k] ? static_cast<int64_t>(a.Hkv) << 32 | n[k] : 0;
     }
-    int64_t inc = sum;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) sum += n[k];
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     at = carry + inc - sum;
     return carry + __shfl_sync(0xffffffffu, inc, 31);
   };
-  int64_t all = 0;
-  for (int base = 0; base < a.B; base += 32 * kEach) all = load(base, all);
-  const int total = static_cast<int>(all);
+  int total = 0;
+  for (int base = 0; base < a.B; base += 32 * kEach) total = load(base, total);
   int x[N];
   targets(total, x);
+  bool found[N];
 #pragma unroll
-  for (int t = 0; t < N; ++t) spot[t] = Spot{a.B, total, static_cast<int>(all >> 32)};
-  int64_t carry = 0;
-  for (int base = 0; base < a.B; base += 32 * kEach) {
+  for (int t = 0; t < N; ++t) {
+    spot[t] = Spot{a.B, total, 0};
+    found[t] = false;
+  }
+  for (int base = 0, carry = 0; base < a.B; base += 32 * kEach) {
     if (a.B > 32 * kEach) carry = load(base, carry);  // else what was loaded still stands
+    unsigned some[kEach];  // lanes whose k-th sequence has rows
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) some[k] = __ballot_sync(0xffffffffu, n[k] > 0);
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      int hit_b = -1;
-      int64_t hit_at = 0, p = at;
+      int hit_k = -1, hit_at = 0, p = at;
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
-        const int b = base + lane * kEach + k, q = static_cast<int>(p);
-        if (x[t] >= 0 ? (x[t] >= q && x[t] < q + n[k]) : b == -1 - x[t]) {
-          hit_b = b;
+        if (x[t] >= 0 ? (x[t] >= p && x[t] < p + n[k]) : base + lane * kEach + k == -1 - x[t]) {
+          hit_k = k;
           hit_at = p;
         }
-        p += n[k] ? static_cast<int64_t>(a.Hkv) << 32 | n[k] : 0;
+        p += n[k];
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, hit_b >= 0);
-      if (hit) {
+      const unsigned hit = __ballot_sync(0xffffffffu, hit_k >= 0);
+      int upto = 32 * kEach;  // of this round, the sequences before the place
+      if (hit && !found[t]) {
         const int src = __ffs(hit) - 1;
-        spot[t].b = __shfl_sync(0xffffffffu, hit_b, src);
-        const int64_t f = __shfl_sync(0xffffffffu, hit_at, src);
-        spot[t].before = static_cast<int>(f);
-        spot[t].units = static_cast<int>(f >> 32);
+        upto = src * kEach + __shfl_sync(0xffffffffu, hit_k, src);
+        spot[t].b = base + upto;
+        spot[t].before = __shfl_sync(0xffffffffu, hit_at, src);
       }
+      if (!found[t]) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int lanes = (upto - k + kEach - 1) / kEach;
+          spot[t].units += a.Hkv * __popc(lanes >= 32 ? some[k] : some[k] & ((1u << lanes) - 1u));
+        }
+      }
+      found[t] |= hit != 0;
     }
   }
   return total;
@@ -521,6 +541,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
+  wait_for_earlier();
+  let_next_start();  // not before: the joining kernel reads the lengths at once
   if (warp == 0) {
     Spot spot[2];
     Share share{0, 0};
@@ -550,7 +572,6 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       s_tiles = n;
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end itself
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -579,7 +600,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     for (int x = 0; x < kQuads; ++x) {
       const int j = 32 * x + q_col;
       raw[x] = QRaw{};
-      if (g0 + q_head < a.gq && j < a.hd) raw[x] = __ldg(reinterpret_cast<const QRaw*>(q + j));
+      if (g0 + q_head < a.gq && j < a.hd) raw[x] = *reinterpret_cast<const QRaw*>(q + j);
     }
   };
   auto query_store = [&](const QRaw* raw, int g0, int qb) {
@@ -824,8 +845,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         auto scales = [&](int k, float* x, float* y) {
           const int r = at + k * 2 * kTile;
           if (first + 2 * k < i1 && r < len) {
-            *x = __ldg(ksp + (r >> lb));
-            *y = __ldg(vsp + (r >> lb));
+            *x = ksp[r >> lb];
+            *y = vsp[r >> lb];
           }
         };
         scales(0, &ks, &vs);
@@ -848,8 +869,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           tc_fence_after();
           float ks2 = 1.f, vs2 = 1.f;
           if (i + 4 < i1 && at + 4 * kTile < len) {
-            ks2 = __ldg(ksp + ((at + 4 * kTile) >> lb));
-            vs2 = __ldg(vsp + ((at + 4 * kTile) >> lb));
+            ks2 = ksp[(at + 4 * kTile) >> lb];
+            vs2 = vsp[(at + 4 * kTile) >> lb];
           }
           float s[GQ];
 #pragma unroll
@@ -998,6 +1019,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   __shared__ __align__(8) float s_red[8][256];
   const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next_start();
+  // the lengths: the attention kernel lets this one start only when what came before it is done
   if (warp == 0) {
     Spot spot;
     const int total = walk_line<1>(a, &spot, [&](int, int* x) { x[0] = -1 - b; });
@@ -1011,7 +1034,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   __syncthreads();
   const int x0 = s_before + h * (nt + 1);
   const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x0 + nt - 1) : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's partials from here on
+  wait_for_earlier();  // the attention's partials from here on
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
     if (blockIdx.y == 0)
@@ -1201,6 +1224,8 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   __shared__ int s_need, s_moves;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % kEvictCtas, unit = blockIdx.x / kEvictCtas, b = unit / a.Hkv;
+  let_next_start();
+  wait_for_earlier();
   const int64_t len = checked_len(a.lens[b], a.capacity, a.status);
   const int n = static_cast<int>((len + a.block - 1) / a.block);
   const bool writes_len = rank == 0 && unit % a.Hkv == 0 && tid == 0;
@@ -1396,16 +1421,40 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
 }  // namespace
 
 // -------------------------------------------------------------- launchers
+// Every kernel here waits (griddepcontrol.wait) before it reads or writes what an
+// earlier one may have written or read, and lets the next one start its own
+// preparation at once: launched programmatically, the calls of a decode step hide
+// each other's launch and set-up.
+template <typename... P, typename... A>
+static xkv_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+}
+
 // Threads and vectors a thread for the rows one block can get: 128 threads up to
 // four vectors each (64 rows of 128), 256 for more.
 template <typename T>
-static void append_typed(const AppendArgs& a, int64_t n_new, int block, unsigned grid, cudaStream_t st) {
+static xkv_status append_typed(const AppendArgs& a, int64_t n_new, int block, unsigned grid, cudaStream_t st) {
   const int vecs = static_cast<int>(std::min<int64_t>(n_new, block)) * a.hd / 16;
-  if (vecs <= 128) kv8_append_kernel<T, 1><<<grid, 128, 0, st>>>(a);
-  else if (vecs <= 256) kv8_append_kernel<T, 2><<<grid, 128, 0, st>>>(a);
-  else if (vecs <= 512) kv8_append_kernel<T, 4><<<grid, 128, 0, st>>>(a);
-  else if (vecs <= 1024) kv8_append_kernel<T, 4><<<grid, 256, 0, st>>>(a);
-  else kv8_append_kernel<T, 8><<<grid, 256, 0, st>>>(a);
+  return vecs <= 128    ? launch(kv8_append_kernel<T, 1>, grid, 128, 0, st, 1, a)
+         : vecs <= 256  ? launch(kv8_append_kernel<T, 2>, grid, 128, 0, st, 1, a)
+         : vecs <= 512  ? launch(kv8_append_kernel<T, 4>, grid, 128, 0, st, 1, a)
+         : vecs <= 1024 ? launch(kv8_append_kernel<T, 4>, grid, 256, 0, st, 1, a)
+                        : launch(kv8_append_kernel<T, 8>, grid, 256, 0, st, 1, a);
 }
 
 xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens,
@@ -1435,9 +1484,8 @@ xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   a.status = device_status_ptr();
   const int64_t grid = static_cast<int64_t>(p->batch) * p->n_kv_heads * 2 * a.nb;
   if (grid > 0x7FFFFFFF) return XKV_ERR_UNSUPPORTED;
-  if (dt == XKV_BF16) append_typed<__nv_bfloat16>(a, n_new, p->block, static_cast<unsigned>(grid), st);
-  else append_typed<float>(a, n_new, p->block, static_cast<unsigned>(grid), st);
-  return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+  return dt == XKV_BF16 ? append_typed<__nv_bfloat16>(a, n_new, p->block, static_cast<unsigned>(grid), st)
+                        : append_typed<float>(a, n_new, p->block, static_cast<unsigned>(grid), st);
 }
 
 KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
@@ -1460,8 +1508,7 @@ static xkv_status attend_tc_shape(const AttendArgs& a, const CUtensorMap* maps, 
   if (cudaFuncSetAttribute(kv8_attend_tc_kernel<T, GQ, HDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return XKV_ERR_CUDA;
-  kv8_attend_tc_kernel<T, GQ, HDA><<<a.ctas, kAttendThreads, smem, st>>>(maps[0], maps[1], a);
-  return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+  return launch(kv8_attend_tc_kernel<T, GQ, HDA>, a.ctas, kAttendThreads, smem, st, 1, maps[0], maps[1], a);
 }
 
 template <typename T>
@@ -1524,17 +1571,8 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
     const int64_t nblk = p->capacity / p->block;
     wy = static_cast<int>(std::min<int64_t>((nblk + kWeightBlocks - 1) / kWeightBlocks, 64));
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units), head_ctas + wy);
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv8_combine_kernel, a, heads, head_ctas) != cudaSuccess) return XKV_ERR_CUDA;
-  return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+  return launch(kv8_combine_kernel, dim3(static_cast<unsigned>(units), head_ctas + wy), kCombineThreads, 0, st, 1, a,
+                heads, head_ctas);
 }
 
 xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens, int budget, int sink,
@@ -1559,23 +1597,11 @@ xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, con
   a.recent = recent;
   a.status = device_status_ptr();
   const size_t smem = static_cast<size_t>((nblk + 31) / 32) * 3 * 4;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads * kEvictCtas);
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kEvictCtas;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(kv8_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kEvictMaxBlocks / 32 * 3 * 4)) != cudaSuccess)
     return XKV_ERR_CUDA;
-  if (cudaLaunchKernelEx(&cfg, kv8_evict_kernel, a) != cudaSuccess) return XKV_ERR_CUDA;
-  return cudaPeekAtLastError() == cudaSuccess ? XKV_OK : XKV_ERR_CUDA;
+  return launch(kv8_evict_kernel, dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads * kEvictCtas), kEvictThreads, smem,
+                st, kEvictCtas, a);
 }
 
 }  // namespace xkv
