@@ -203,7 +203,8 @@ struct AttendArgs {
   const float* v_scale;
   const void* q;
   const int32_t* lens;
-  float* part;   // partial slots: [gq][hd] sums, [gq] references, [4][gq] softmax sums of a warp's rows
+  float* part;   // partial slots: [gq][hd] sums
+  float2* ml;    // [slot][gq] their references and softmax sums
   float* wpart;  // [unit][tile][sub-block][gq] sums of the tile's weights, or NULL
   float* wref;   // [unit][tile][gq] the maxima they refer to
   float* weight;
@@ -214,8 +215,6 @@ struct AttendArgs {
   int* status;
 };
 
-// a multiple of four, so that a slot's columns can be read in pairs
-__host__ __device__ inline int slot_floats(int gq, int hd) { return (gq * (hd + 5) + 3) & ~3; }
 __host__ __device__ inline int sub_rows(int block) { return block < 32 ? block : 32; }
 
 // Units' tiles stand in one line (sequence, head, tile), and CTA c of n takes a
@@ -507,7 +506,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ Walk s_walk;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
-  __shared__ float s_qc[kAhead][GQ];
+  __shared__ float s_qc[kAhead][GQ], s_sum[2][2][4][GQ];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sm;
   uint8_t* sv = sk + kStages * HDA * kAtom;
@@ -969,23 +968,20 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         if (first < i1) {
           // the unit's partial of this warpgroup
           fold(((i1 - 1 - wg) & ~1) / 2);
-          float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * slot_floats(a.gq, a.hd);
+          float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * (a.gq * a.hd);
 #pragma unroll
           for (int g = 0; g < GQ; ++g)
 #pragma unroll
             for (int x = 0; x < HDA; ++x)
               if (g < a.gq && row + 128 * x < a.hd) slot[g * a.hd + row + 128 * x] = acc[x][g];
-          slot += a.gq * a.hd;
-          group_sums<GQ>(l, 32, [&](int g, float sum) {
-            if (g < a.gq) slot[(1 + quarter) * a.gq + g] = sum;
-          });
-          if (row < a.gq) slot[row] = m;
-        }
-        if (first >= i1 && row < a.gq) {  // no tile of the unit: a slot that weighs nothing
-          float* slot = a.part + (2 * (unit + blockIdx.x) + wg) * slot_floats(a.gq, a.hd) + a.gq * a.hd + row;
-          slot[0] = -INFINITY;
-#pragma unroll
-          for (int k = 1; k < 5; ++k) slot[k * a.gq] = 0.f;
+          float(*sums)[GQ] = s_sum[wg][seg & 1];  // read before the warpgroup's barrier after next
+          group_sums<GQ>(l, 32, [&](int g, float sum) { sums[quarter][g] = sum; });
+          named_bar_sync(1 + wg, 128);
+          if (row < a.gq)
+            a.ml[(2 * (unit + blockIdx.x) + wg) * a.gq + row] =
+                make_float2(m, (sums[0][row] + sums[1][row]) + (sums[2][row] + sums[3][row]));
+        } else if (row < a.gq) {  // no tile of the unit: a slot that weighs nothing
+          a.ml[(2 * (unit + blockIdx.x) + wg) * a.gq + row] = make_float2(-INFINITY, 0.f);
         }
         // to the next unit
         i0 = i1;
@@ -1042,21 +1038,21 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
     return;
   }
   // the unit's slots: two for each CTA whose share meets it
-  const int sf = slot_floats(gq, hd), slots = 2 * (c1 - c0 + 1);
+  const int sf = gq * hd, slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
   // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M)
   auto head = [&](int g, float* f) {
     constexpr int kHeld = 2;  // slots a lane holds: 64 in all, the rest in further rounds
-    const float* s = base + gq * hd + g;
+    const float2* ml = a.ml + 2 * static_cast<int64_t>(unit + c0) * gq + g;
     float M = -INFINITY, L = 0.f;
     for (int from = 0; from < slots; from += 32 * kHeld) {
       float m[kHeld], l[kHeld];
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) {
         const int k = from + 32 * e + lane;
-        const float* x = s + static_cast<int64_t>(k) * sf;
-        m[e] = k < slots ? x[0] : -INFINITY;
-        l[e] = k < slots ? (x[gq] + x[2 * gq]) + (x[3 * gq] + x[4 * gq]) : 0.f;
+        const float2 x = k < slots ? ml[static_cast<int64_t>(k) * gq] : make_float2(-INFINITY, 0.f);
+        m[e] = x.x;
+        l[e] = x.y;
       }
       float top = M;
 #pragma unroll
@@ -1083,24 +1079,43 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   };
   if (static_cast<int>(blockIdx.y) < head_ctas) {
     const int wph = 8 / heads, slot = warp / wph, part = warp % wph, g = blockIdx.y * heads + slot;
-    if (part == 0 && g < gq) head(g, s_f[slot]);
-    __syncthreads();
     const int pairs = hd / 2;  // a lane's columns come in pairs, 64 columns apart
+    const float2* sums = reinterpret_cast<const float2*>(base + g * hd);
+    constexpr int kHeld = 4;  // slots whose sums a warp has in hand at a time, the first of them before it knows their factors
+    float2 v[kHeld][4];
+    auto load = [&](int from) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const int k = from + j * wph;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[j][e] = k < slots && e * 32 + lane < pairs
+                        ? *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sums) +
+                                                           static_cast<int64_t>(k) * sf + 2 * (e * 32 + lane))
+                        : make_float2(0.f, 0.f);
+      }
+    };
+    if (g < gq) {
+      load(part);
+      if (part == 0) head(g, s_f[slot]);
+    }
+    __syncthreads();
     if (g < gq) {
       float2 acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int k = part; k < slots; k += wph) {
-        const float f = s_f[slot][k];
-        const float2* s = reinterpret_cast<const float2*>(base + static_cast<int64_t>(k) * sf + g * hd);
+      for (int from = part; from < slots; from += kHeld * wph) {
+        if (from != part) load(from);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = e * 32 + lane;
-          // a slot without rows holds anything
-          const float2 v = f != 0.f && col < pairs ? s[col] : make_float2(0.f, 0.f);
-          acc[e].x = fmaf(f, v.x, acc[e].x);
-          acc[e].y = fmaf(f, v.y, acc[e].y);
+        for (int j = 0; j < kHeld; ++j) {
+          const int k = from + j * wph;
+          const float f = k < slots ? s_f[slot][k] : 0.f;
+          if (f == 0.f) continue;  // a slot without rows holds anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
+            acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
+          }
         }
       }
 #pragma unroll
@@ -1117,18 +1132,16 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
     }
     return;
   }
-  for (int g = warp; g < gq; g += 8) head(g, nullptr);
-  __syncthreads();
-  // sixteen threads (heads) to a block, four blocks a thread
+  // sixteen threads (heads) to a block, four blocks a thread; the first blocks' sums are in flight while the heads'
+  // own are found
   const int nblk = static_cast<int>(a.capacity / a.block), n = (len + a.block - 1) / a.block;
   const int sub = sub_rows(a.block), spb = a.block / sub, per_tile = kTile / a.block;
   const int g = tid & 15;
-  const float mg = g < gq ? s_m[g] : 0.f, rg = g < gq ? s_r[g] : 0.f;
   const float* ref = a.wref + static_cast<int64_t>(unit) * a.tiles_cap * gq + g;
   const float* p = a.wpart + static_cast<int64_t>(unit) * a.tiles_cap * (kTile / sub) * gq + g;
   float* weight = a.weight + static_cast<int64_t>(unit) * nblk;
-  for (int k0 = (blockIdx.y - head_ctas) * kWeightBlocks; k0 < n; k0 += (gridDim.y - head_ctas) * kWeightBlocks) {
-    float r[4], v[4][4], old[4];
+  float r[4], v[4][4], old[4];
+  auto load = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + 16 * j + (tid >> 4);
@@ -1138,6 +1151,15 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[j][e] = in && e < spb ? p[(static_cast<int64_t>(k) * spb + e) * gq] : 0.f;
     }
+  };
+  const int first = (blockIdx.y - head_ctas) * kWeightBlocks;
+  if (first >= n) return;
+  load(first);
+  for (int h8 = warp; h8 < gq; h8 += 8) head(h8, nullptr);
+  __syncthreads();
+  const float mg = g < gq ? s_m[g] : 0.f, rg = g < gq ? s_r[g] : 0.f;
+  for (int k0 = first; k0 < n; k0 += (gridDim.y - head_ctas) * kWeightBlocks) {
+    if (k0 != first) load(k0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + 16 * j + (tid >> 4);
@@ -1496,7 +1518,8 @@ KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
   r.ctas = std::min(num_sms(), kMaxSlots / 2);
   const int spt = kTile / sub_rows(p->block);
   const size_t slots = 2 * static_cast<size_t>(units + r.ctas);
-  r.off_wpart = align_up(slots * slot_floats(gq, hd) * 4);
+  r.off_ml = align_up(slots * gq * hd * 4);
+  r.off_wpart = r.off_ml + align_up(slots * gq * 8);
   r.off_wref = r.off_wpart + align_up(static_cast<size_t>(units) * r.tiles_cap * spt * gq * 4);
   r.bytes = r.off_wref + align_up(static_cast<size_t>(units) * r.tiles_cap * gq * 4);
   return r;
@@ -1534,6 +1557,7 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   a.lens = lens;
   char* w = static_cast<char*>(ws);
   a.part = reinterpret_cast<float*>(w);
+  a.ml = reinterpret_cast<float2*>(w + plan.off_ml);
   if (accumulate) {
     a.wpart = reinterpret_cast<float*>(w + plan.off_wpart);
     a.wref = reinterpret_cast<float*>(w + plan.off_wref);
