@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   __shared__ int s_before, s_total;
   __shared__ float s_f[8][kMaxSlots];
   __shared__ float s_m[16], s_r[16];
-  __shared__ __align__(8) float s_red[8][256];
+  __shared__ __align__(16) float s_red[8][256];
   const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_start();
@@ -1043,14 +1043,14 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M)
   auto head = [&](int g, float* f) {
     constexpr int kHeld = 2;  // slots a lane holds: 64 in all, the rest in further rounds
-    const float2* ml = a.ml + 2 * static_cast<int64_t>(unit + c0) * gq + g;
+    const float2* ml = a.ml + 2 * static_cast<int64_t>(unit + c0) * gq + g;  // below 2^31 from here on: 512 slots
     float M = -INFINITY, L = 0.f;
     for (int from = 0; from < slots; from += 32 * kHeld) {
       float m[kHeld], l[kHeld];
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) {
         const int k = from + 32 * e + lane;
-        const float2 x = k < slots ? ml[static_cast<int64_t>(k) * gq] : make_float2(-INFINITY, 0.f);
+        const float2 x = k < slots ? ml[k * gq] : make_float2(-INFINITY, 0.f);
         m[e] = x.x;
         l[e] = x.y;
       }
@@ -1079,20 +1079,18 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   };
   if (static_cast<int>(blockIdx.y) < head_ctas) {
     const int wph = 8 / heads, slot = warp / wph, part = warp % wph, g = blockIdx.y * heads + slot;
-    const int pairs = hd / 2;  // a lane's columns come in pairs, 64 columns apart
-    const float2* sums = reinterpret_cast<const float2*>(base + g * hd);
-    constexpr int kHeld = 4;  // slots whose sums a warp has in hand at a time, the first of them before it knows their factors
-    float2 v[kHeld][4];
+    // a lane has four columns, and four more 128 columns on; the first slots' sums are loaded before their factors
+    // are known
+    constexpr int kHeld = 4;
+    const float* sums = base + g * hd + 4 * lane;
+    const bool lo = 4 * lane < hd, hi = 4 * lane + 128 < hd;
+    float4 v[kHeld], z[kHeld];
     auto load = [&](int from) {
 #pragma unroll
       for (int j = 0; j < kHeld; ++j) {
         const int k = from + j * wph;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[j][e] = k < slots && e * 32 + lane < pairs
-                        ? *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sums) +
-                                                           static_cast<int64_t>(k) * sf + 2 * (e * 32 + lane))
-                        : make_float2(0.f, 0.f);
+        if (lo && k < slots) v[j] = *reinterpret_cast<const float4*>(sums + k * sf);
+        if (hi && k < slots) z[j] = *reinterpret_cast<const float4*>(sums + k * sf + 128);
       }
     };
     if (g < gq) {
@@ -1101,9 +1099,13 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
     }
     __syncthreads();
     if (g < gq) {
-      float2 acc[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      auto add = [](float4& s, float f, const float4& t) {
+        s.x = fmaf(f, t.x, s.x);
+        s.y = fmaf(f, t.y, s.y);
+        s.z = fmaf(f, t.z, s.z);
+        s.w = fmaf(f, t.w, s.w);
+      };
       for (int from = part; from < slots; from += kHeld * wph) {
         if (from != part) load(from);
 #pragma unroll
@@ -1111,21 +1113,17 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
           const int k = from + j * wph;
           const float f = k < slots ? s_f[slot][k] : 0.f;
           if (f == 0.f) continue;  // a slot without rows holds anything
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
-            acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
-          }
+          add(x, f, v[j]);
+          if (hi) add(y, f, z[j]);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e * 32 + lane < pairs) *reinterpret_cast<float2*>(&s_red[warp][2 * (e * 32 + lane)]) = acc[e];
+      if (lo) *reinterpret_cast<float4*>(&s_red[warp][4 * lane]) = x;
+      if (hi) *reinterpret_cast<float4*>(&s_red[warp][4 * lane + 128]) = y;
     }
     __syncthreads();
-    for (int i = tid; i < heads * hd; i += kCombineThreads) {
-      const int hh = i / hd, col = i % hd, gg = blockIdx.y * heads + hh;
-      if (gg >= gq) break;
+    for (int i = tid; i < heads * 256; i += kCombineThreads) {
+      const int hh = i >> 8, col = i & 255, gg = blockIdx.y * heads + hh;
+      if (gg >= gq || col >= hd) continue;
       float o = 0.f;
       for (int k = 0; k < wph; ++k) o += s_red[hh * wph + k][col];
       out[gg * hd + col] = o * s_r[gg];
@@ -1134,22 +1132,22 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   }
   // sixteen threads (heads) to a block, four blocks a thread; the first blocks' sums are in flight while the heads'
   // own are found
-  const int nblk = static_cast<int>(a.capacity / a.block), n = (len + a.block - 1) / a.block;
-  const int sub = sub_rows(a.block), spb = a.block / sub, per_tile = kTile / a.block;
+  const int lb = 31 - __clz(a.block), n = (len + a.block - 1) >> lb;
+  const int ls = min(lb, 5), spb = 1 << (lb - ls);  // a block's sub-blocks
   const int g = tid & 15;
   const float* ref = a.wref + static_cast<int64_t>(unit) * a.tiles_cap * gq + g;
-  const float* p = a.wpart + static_cast<int64_t>(unit) * a.tiles_cap * (kTile / sub) * gq + g;
-  float* weight = a.weight + static_cast<int64_t>(unit) * nblk;
+  const float* p = a.wpart + static_cast<int64_t>(unit) * a.tiles_cap * (kTile >> ls) * gq + g;
+  float* weight = a.weight + static_cast<int64_t>(unit) * (a.capacity >> lb);
   float r[4], v[4][4], old[4];
   auto load = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + 16 * j + (tid >> 4);
       const bool in = g < gq && k < n;
-      r[j] = in ? ref[static_cast<int64_t>(k / per_tile) * gq] : 0.f;
+      r[j] = in ? ref[(k >> (7 - lb)) * gq] : 0.f;
       old[j] = k < n ? weight[k] : 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[j][e] = in && e < spb ? p[(static_cast<int64_t>(k) * spb + e) * gq] : 0.f;
+      for (int e = 0; e < 4; ++e) v[j][e] = in && e < spb ? p[static_cast<int64_t>(k * spb + e) * gq] : 0.f;
     }
   };
   const int first = (blockIdx.y - head_ctas) * kWeightBlocks;
