@@ -513,26 +513,25 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   uint8_t* sp = sv + kStages * HDA * kAtom;
   uint8_t* sq = sp + Sh::bytes_p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+  if (warp == kWarpO) {  // while warp 0 finds the share
+    if (lane < kStages) {
+      mbar_init(&k_full[lane], 1);
+      mbar_init(&k_empty[lane], 1);
+      mbar_init(&v_full[lane], 1);
+      mbar_init(&v_empty[lane], 1);
     }
-    for (int i = 0; i < kAhead; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
-      mbar_init(&q_full[i], 32);
-      mbar_init(&q_empty[i], 1 + 256);
+    if (lane < kAhead) {
+      mbar_init(&s_full[lane], 1);
+      mbar_init(&s_empty[lane], 4);
+      mbar_init(&q_full[lane], 32);
+      mbar_init(&q_empty[lane], 1 + 256);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
+    if (lane < 2) {
+      mbar_init(&p_full[lane], 128);
+      mbar_init(&o_full[lane], 1);
+      mbar_init(&done[lane], 1);
     }
-    mbar_init(&done[0], 1);
-    mbar_init(&done[1], 1);
-    s_abort = 0;
+    if (lane == 0) s_abort = 0;
     fence_mbar_init();
   }
   if (warp == kWarpS) tmem_alloc(&s_tmem, Sh::tmem);
@@ -1181,7 +1180,7 @@ struct EvictArgs {
   int Hkv, hd, block, budget, sink, recent;
   int* status;
 };
-constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit
+constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit; those of sequences within the budget leave at once
 constexpr int kEvictThreads = 256;
 constexpr int64_t kEvictMaxBlocks = 131072;  // three bit-mask arrays of a unit's blocks in shared memory
 
@@ -1241,7 +1240,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   extern __shared__ uint32_t s_dyn[];
   __shared__ uint32_t s_hist[2][256];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need, s_moves;
+  __shared__ int s_need, s_moves, s_whole;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % kEvictCtas, unit = blockIdx.x / kEvictCtas, b = unit / a.Hkv;
   let_next_start();
@@ -1293,10 +1292,12 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   if (tid == 0) {
     s_prefix = 0;
     s_need = a.budget;
+    s_whole = 0;
   }
   s_hist[0][tid] = 0;
   __syncthreads();
-  for (int pass = 0; pass < 4; ++pass) {
+  // done early where every key of the last bin is kept: two passes, as a rule, for weights without ties
+  for (int pass = 0; pass < 4 && !s_whole; ++pass) {
     const int shift = 24 - 8 * pass;
     uint32_t* hist = s_hist[pass & 1];
     const uint32_t prefix = s_prefix, mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
@@ -1328,6 +1329,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
           if (above < need && above + c[k] >= need) {
             s_prefix = prefix | static_cast<uint32_t>(255 - 8 * lane - k) << shift;
             s_need = static_cast<int>(need - above);
+            s_whole = need - above == c[k];
             above = 0xFFFFFFFFu;
           } else if (above != 0xFFFFFFFFu) {
             above += c[k];
@@ -1337,15 +1339,17 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
     }
     __syncthreads();
   }
-  // bit masks: keys above the threshold, and of those equal to it the lowest `need`
+  // bit masks: keys above the threshold, and of those equal to it the lowest `need`; or, where a bin is kept as a
+  // whole, all keys from its first on
   const uint32_t threshold = s_prefix;
   const int need = s_need;
+  const bool whole = s_whole;
   const int nw = (n + 31) / 32;
   uint32_t* keep = s_dyn;
   int* pref_m = reinterpret_cast<int*>(s_dyn + nw);
   uint32_t* equal = s_dyn + 2 * nw;
   each([&](int i, uint32_t u) {
-    const unsigned gt = __ballot_sync(0xffffffffu, i < n && u > threshold);
+    const unsigned gt = __ballot_sync(0xffffffffu, i < n && (u > threshold || (whole && u == threshold)));
     const unsigned eq = __ballot_sync(0xffffffffu, i < n && u == threshold);
     if (lane == 0 && i < n) {
       keep[i >> 5] = gt;
@@ -1355,19 +1359,21 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   // this CTA has read weights and numbers: others may change them once all have
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   __syncthreads();
-  if (warp == 0) warp_scan(nw, pref_m, [&](int w) { return __popc(equal[w]); });
-  __syncthreads();
-  for (int w = tid; w < nw; w += kEvictThreads) {
-    int take = need - pref_m[w];
-    uint32_t eq = equal[w], add = 0;
-    while (take > 0 && eq) {
-      add |= eq & (0u - eq);
-      eq &= eq - 1;
-      --take;
+  if (!whole) {
+    if (warp == 0) warp_scan(nw, pref_m, [&](int w) { return __popc(equal[w]); });
+    __syncthreads();
+    for (int w = tid; w < nw; w += kEvictThreads) {
+      int take = need - pref_m[w];
+      uint32_t eq = equal[w], add = 0;
+      while (take > 0 && eq) {
+        add |= eq & (0u - eq);
+        eq &= eq - 1;
+        --take;
+      }
+      keep[w] |= add;
     }
-    keep[w] |= add;
+    __syncthreads();
   }
-  __syncthreads();
   // movers: kept, slot >= budget - 1; free: not kept, slot < budget - 1, and slot budget - 1
   const int edge = a.budget - 1, we = edge / 32;
   const uint32_t below = (1u << (edge & 31)) - 1u;
@@ -1390,49 +1396,35 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
     *dst = wf * 32 + nth_bit(empty(wf), r - pref_f[wf]);
   };
   // the codes in pieces of 32 x 8 vectors, dealt out to the cluster's warps, a piece's loads in flight together
-  constexpr int kWarps = kEvictCtas * kEvictThreads / 32;
   const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
+  constexpr int kWarps = kEvictCtas * kEvictThreads / 32;
   const int me = warp * kEvictCtas + rank;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int64_t w = me; w < static_cast<int64_t>(rounds) * 2 * per; w += kWarps) {
     const int r = static_cast<int>(w / (2 * per)), q = static_cast<int>(w - static_cast<int64_t>(r) * 2 * per);
     const int x = q >= per, first = (x ? q - per : q) * 256 + lane;
     int src, dst;
     place(r, &src, &dst);
     uint4* rows = reinterpret_cast<uint4*>((x ? a.code[1] : a.code[0]) + unit * a.capacity * a.hd) + first;
-    uint4 v[8], z[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (first + 32 * k < nv) v[k] = rows[static_cast<int64_t>(src) * nv + 32 * k];
-    if (r == 0 && pair) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (first + 32 * k < nv) z[k] = rows[static_cast<int64_t>(n - 1) * nv + 32 * k];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + 32 * k] = v[k];
+    // with a block's first piece go its scale and its weight (K) or number (V), by the first two lanes
+    uint32_t* tail = lane == 0 ? reinterpret_cast<uint32_t*>(x ? a.scale[1] : a.scale[0])
+                     : x       ? reinterpret_cast<uint32_t*>(a.ids)
+                               : reinterpret_cast<uint32_t*>(a.weight);
+    tail += unit * nblk;
+    const bool tails = (x ? q - per : q) == 0 && lane < 2;
+    for (;;) {
+      uint4 v[8];
+      const uint32_t t = tails ? tail[src] : 0u;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (first + 32 * k < nv) rows[static_cast<int64_t>(edge) * nv + 32 * k] = z[k];
-    } else {
+        if (first + 32 * k < nv) v[k] = rows[static_cast<int64_t>(src) * nv + 32 * k];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + 32 * k] = v[k];
-    }
-  }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  // scales, weights and numbers: lane l < 4 has one of the four arrays
-  for (int r = me; r < rounds; r += kWarps) {
-    int src, dst;
-    place(r, &src, &dst);
-    if (lane < 4) {
-      uint32_t* x = lane == 0   ? reinterpret_cast<uint32_t*>(a.scale[0])
-                    : lane == 1 ? reinterpret_cast<uint32_t*>(a.scale[1])
-                    : lane == 2 ? reinterpret_cast<uint32_t*>(a.weight)
-                                : reinterpret_cast<uint32_t*>(a.ids);
-      x += unit * nblk;
-      const uint32_t v = x[src], z = x[n - 1];
-      x[dst] = v;
-      if (r == 0 && pair) x[edge] = z;
+      if (tails) tail[dst] = t;
+      if (r > 0 || !pair || src == n - 1) break;
+      src = n - 1;
+      dst = edge;
     }
   }
   if (writes_len) a.lens_out[b] = static_cast<int32_t>(len - static_cast<int64_t>(n - a.budget) * a.block);
