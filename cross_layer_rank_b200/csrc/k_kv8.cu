@@ -534,13 +534,14 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     if (lane == 0) s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpS) tmem_alloc(&s_tmem, Sh::tmem);
   if (warp == kWarpTma && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
   wait_for_earlier();
   let_next_start();  // not before: the joining kernel reads the lengths at once
+  // nor TMEM, which an earlier kernel on this SM may still ask for while this one waits for it
+  if (warp == kWarpS) tmem_alloc(&s_tmem, Sh::tmem);
   if (warp == 0) {
     Spot spot[2];
     Share share{0, 0};
@@ -1592,7 +1593,8 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
 xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens, int budget, int sink,
                             int recent, int32_t* lens_out, cudaStream_t st) {
   const int64_t nblk = p->capacity / p->block;
-  if (nblk > kEvictMaxBlocks) return XKV_ERR_UNSUPPORTED;
+  if (nblk > kEvictMaxBlocks || static_cast<int64_t>(p->batch) * p->n_kv_heads * kEvictCtas > 0x7FFFFFFF)
+    return XKV_ERR_UNSUPPORTED;
   EvictArgs a{};
   a.code[0] = static_cast<uint8_t*>(c->k);
   a.code[1] = static_cast<uint8_t*>(c->v);

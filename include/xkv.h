@@ -495,7 +495,8 @@ XKV_API xkv_status xkv_kv8_attention_decode(const xkv_kv8_params* p, const xkv_k
  * after it, lens[b] - (n - budget) block for n = ceil(lens[b] / block) > budget;
  * lens_out may not overlap lens.
  * Requires 1 <= recent, 0 <= sink, sink + recent <= budget, weight and ids; at
- * most 131072 blocks per sequence (else XKV_ERR_UNSUPPORTED). */
+ * most 131072 blocks per sequence and 2^28 - 1 (sequence, KV head) pairs (else
+ * XKV_ERR_UNSUPPORTED). */
 XKV_API xkv_status xkv_kv8_evict(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens, int budget,
                                  int sink, int recent, int32_t* lens_out, void* stream);
 

@@ -469,6 +469,45 @@ def test_graphs_streams_and_a_shared_workspace(xkv):
     assert xkv.get_device_status() == 0
 
 
+def _chain(xkv, seed, steps, wait):
+    """Steps of append, attention with weights and eviction, one behind the other; every output and the last cache."""
+    B, H, gq, hd, block, budget = 5, 2, 8, 64, 16, 9
+    g = torch.Generator().manual_seed(seed)
+    b, _ = _fill(xkv, B, H, hd, block, 192, [100, 1, 40, 144, 0], seed=seed)
+    k = torch.randn((steps, B, 3, H * hd), generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn((steps, B, H * gq, hd), generator=g).to(torch.bfloat16).cuda()
+    outs = torch.full((steps, B, H * gq, hd), float("nan"), device="cuda")
+    ws = xkv.workspace(xkv.xkv_kv8_workspace_size(b.p, H * gq))
+    lens, after = b.dev_lens(), torch.empty(B, dtype=torch.int32, device="cuda")
+    b.c.weight.nan_to_num_()
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for call in (lambda: xkv.xkv_kv8_append(b.p, b.c, lens, k[i], k[i].flip(0)), lambda: lens.add_(3),
+                     lambda: xkv.xkv_kv8_attention_decode(b.p, b.c, lens, q[i], outs[i], accumulate=True, ws=ws),
+                     lambda: xkv.xkv_kv8_evict(b.p, b.c, lens, budget, 1, 2, after), lambda: lens.copy_(after)):
+            call()
+            if wait:
+                torch.cuda.synchronize()
+    return [outs, lens, b.c.k.view(torch.uint8), b.c.v.view(torch.uint8), b.c.k_scale, b.c.weight, b.c.ids]
+
+
+def test_calls_behind_one_another_and_side_by_side(xkv):
+    # nothing waits between the calls, which prepare themselves while the one before still runs; then two such runs
+    # on streams of their own
+    want = [[t.clone() for t in _chain(xkv, seed, 60, True)] for seed in (1, 2)]
+    for got, ref_ in ((_chain(xkv, 1, 60, False), want[0]), (_chain(xkv, 2, 60, False), want[1])):
+        torch.cuda.synchronize()
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(got, ref_))
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for s, seed in zip(streams, (1, 2)):
+        with torch.cuda.stream(s):
+            got.append(_chain(xkv, seed, 60, False))
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert all(torch.equal(u.view(torch.uint8), v.view(torch.uint8)) for u, v in zip(x, y))
+    assert xkv.get_device_status() == 0
+
+
 def test_binding_refuses_what_the_library_cannot_see(xkv):
     b, g = _fill(xkv, 2, 2, 64, 16, 64, [10, 20])
     q, out = torch.zeros((2, 4, 64), device="cuda"), torch.empty((2, 4, 64), device="cuda")

@@ -92,6 +92,8 @@ def test_attention_and_eviction_arguments(xkv):
     for gone in ("weight", "ids"):
         assert g(p, _c(xkv, **{gone: None}), FAKE, 4, 1, 1, far, None) == inv
     assert g(_p(xkv, block=8, capacity=8 * 131073), c, FAKE, 4, 1, 1, far, None) == xkv.XKV_ERR_UNSUPPORTED
+    assert g(_p(xkv, batch=1 << 28, n_kv_heads=1, block=8, capacity=8), c, FAKE, 1, 0, 1, C.c_void_p(1 << 40),
+             None) == xkv.XKV_ERR_UNSUPPORTED
 
 
 def test_binding_checks_the_cache_tensors(xkv):
