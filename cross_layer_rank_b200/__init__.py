@@ -494,16 +494,18 @@ class KV8Cache:
                    torch.empty(nblk, dtype=torch.int32, device=device))
 
 
-def _kv8_check(p: KV8Params, cache: KV8Cache, *tensors):
-    """What the C call cannot see: the cache is p's and everything lies on the current device."""
+def _kv8_check(p: KV8Params, cache: KV8Cache, stream, *tensors):
+    """What the C call cannot see: the cache is p's and everything lies on the current device.
+    Returns the stream, the device's current one where none is given."""
     if cache.sizes != (p.batch, p.n_kv_heads, p.capacity, p.head_dim, p.block):
         raise ValueError("the cache's tensors do not have p's sizes")
     device = cache.index
     if device != torch.cuda.current_device():
         raise ValueError("the cache is not on the current CUDA device")
     for t in tensors:
-        if t is not None and t.get_device() != device:
+        if t.get_device() != device:
             raise ValueError("all tensors must be on the cache's device")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _lens_ptr(p: KV8Params, t):
@@ -517,7 +519,7 @@ def _lens_ptr(p: KV8Params, t):
 def xkv_kv8_append(p: KV8Params, cache: KV8Cache, lens, k_new, v_new, counts=None, stream=None):
     """Round new rows k_new, v_new [B][n][Hkv hd] (views with contiguous rows are accepted) into the
     cache at positions lens[b] ...; counts[b] <= n rows where given.  lens is not advanced."""
-    _kv8_check(p, cache, lens, k_new, v_new, counts)
+    stream = _kv8_check(p, cache, stream, lens, k_new, v_new, lens if counts is None else counts)
     shape, strides, dtype = k_new.shape, k_new.stride(), k_new.dtype
     if len(shape) != 3 or v_new.shape != shape or v_new.dtype != dtype or shape[0] != p.batch or \
             shape[2] != p.n_kv_heads * p.head_dim:
@@ -528,7 +530,7 @@ def xkv_kv8_append(p: KV8Params, cache: KV8Cache, lens, k_new, v_new, counts=Non
     _check(lib.xkv_kv8_append(p, cache.pointers, _lens_ptr(p, lens), _lens_ptr(p, counts), shape[1],
                               dtype_code(dtype), k_new.data_ptr(), v_new.data_ptr(),
                               strides[1] if shape[1] > 1 else shape[2], strides[0] if shape[0] > 1 else 0,
-                              _stream(stream)), "xkv_kv8_append")
+                              stream), "xkv_kv8_append")
 
 
 def xkv_kv8_workspace_size(p: KV8Params, n_q_heads: int) -> int:
@@ -539,24 +541,26 @@ def xkv_kv8_attention_decode(p: KV8Params, cache: KV8Cache, lens, q, out, accumu
                              stream=None):
     """One decode step over the 8-bit cache; writes out [B][Hq][hd] f32 and, with accumulate, adds
     every block's attention weight to cache.weight."""
-    _kv8_check(p, cache, lens, q, out, ws)
+    if ws is None:
+        ws = workspace(xkv_kv8_workspace_size(p, q.shape[1] if q.dim() == 3 else 0), q.device)
+    stream = _kv8_check(p, cache, stream, lens, q, out, ws)
     shape = q.shape
     if len(shape) != 3 or shape[0] != p.batch or shape[2] != p.head_dim or out.shape != shape or \
             out.dtype != torch.float32:
         raise ValueError("q is [B][Hq][hd] and out the same shape in float32")
-    n_q_heads = shape[1]
-    ws = ws if ws is not None else workspace(xkv_kv8_workspace_size(p, n_q_heads), q.device)
-    _check(lib.xkv_kv8_attention_decode(p, cache.pointers, _lens_ptr(p, lens), n_q_heads, dtype_code(q.dtype), _ptr(q),
-                                        _ptr(out), int(bool(accumulate)), _ptr(ws), ws.numel() * ws.element_size(),
-                                        _stream(stream)), "xkv_kv8_attention_decode")
+    if not (q.is_contiguous() and out.is_contiguous() and ws.is_contiguous()):
+        raise ValueError("expected contiguous tensors")
+    _check(lib.xkv_kv8_attention_decode(p, cache.pointers, _lens_ptr(p, lens), shape[1], dtype_code(q.dtype),
+                                        q.data_ptr(), out.data_ptr(), 1 if accumulate else 0, ws.data_ptr(),
+                                        ws.numel() * ws.element_size(), stream), "xkv_kv8_attention_decode")
 
 
 def xkv_kv8_evict(p: KV8Params, cache: KV8Cache, lens, budget: int, sink: int, recent: int, lens_out, stream=None):
     """Keep `budget` blocks of every longer sequence and KV head: the first `sink`, the newest
     `recent` and those with the most weight.  lens_out receives the lengths after it."""
-    _kv8_check(p, cache, lens, lens_out)
+    stream = _kv8_check(p, cache, stream, lens, lens_out)
     _check(lib.xkv_kv8_evict(p, cache.pointers, _lens_ptr(p, lens), budget, sink, recent, _lens_ptr(p, lens_out),
-                             _stream(stream)), "xkv_kv8_evict")
+                             stream), "xkv_kv8_evict")
 
 
 # -------------------------------------------------------------------- NER
