@@ -1189,9 +1189,10 @@ struct EvictArgs {
   int32_t* lens_out;
   int64_t capacity;
   int Hkv, hd, block, budget, sink, recent;
+  int ctas;  // of a unit's cluster
   int* status;
 };
-constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit; those of sequences within the budget leave at once
+constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit at most; those of sequences within the budget leave at once
 constexpr int kEvictThreads = 256;
 constexpr int64_t kEvictMaxBlocks = 131072;  // three bit-mask arrays of a unit's blocks in shared memory
 
@@ -1253,7 +1254,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, s_moves, s_whole;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x % kEvictCtas, unit = blockIdx.x / kEvictCtas, b = unit / a.Hkv;
+  const int rank = blockIdx.x % a.ctas, unit = blockIdx.x / a.ctas, b = unit / a.Hkv;
   let_next_start();
   wait_for_earlier();
   const int64_t len = checked_len(a.lens[b], a.capacity, a.status);
@@ -1408,10 +1409,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   };
   // the codes in pieces of 32 x 8 vectors, dealt out to the cluster's warps, a piece's loads in flight together
   const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
-  constexpr int kWarps = kEvictCtas * kEvictThreads / 32;
-  const int me = warp * kEvictCtas + rank;
+  const int warps = a.ctas * kEvictThreads / 32, me = warp * a.ctas + rank;
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int64_t w = me; w < static_cast<int64_t>(rounds) * 2 * per; w += kWarps) {
+  for (int64_t w = me; w < static_cast<int64_t>(rounds) * 2 * per; w += warps) {
     const int r = static_cast<int>(w / (2 * per)), q = static_cast<int>(w - static_cast<int64_t>(r) * 2 * per);
     const int x = q >= per, first = (x ? q - per : q) * 256 + lane;
     int src, dst;
@@ -1631,8 +1631,14 @@ xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, con
   if (cudaFuncSetAttribute(kv8_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kEvictMaxBlocks / 32 * 3 * 4)) != cudaSuccess)
     return XKV_ERR_CUDA;
-  return launch(kv8_evict_kernel, dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads * kEvictCtas), kEvictThreads, smem,
-                st, kEvictCtas, a);
+  // CTAs to a unit: up to eight, as long as each warp can get two pieces of the most blocks that can move.  A CTA of
+  // its own costs each the selection; with eight for every unit, 144 units of 9 blocks took 17 us, with one 6 us.
+  const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(nblk - budget + 1, 1));
+  const int64_t pieces = 2 * moves * ((p->block * p->head_dim / 16 + 255) / 256);
+  a.ctas = 1;
+  while (a.ctas < kEvictCtas && pieces > 2 * a.ctas * (kEvictThreads / 32)) a.ctas *= 2;
+  return launch(kv8_evict_kernel, dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads * a.ctas), kEvictThreads, smem, st,
+                a.ctas, a);
 }
 
 }  // namespace xkv
