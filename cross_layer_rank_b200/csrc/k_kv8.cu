@@ -374,9 +374,11 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) {
 
 // The small operands as several e4m3 ones.
 // Queries: x = sum_i 16^-i piece_i.  A piece holds four significant bits and
-// leaves a remainder of at most 2^-4 of itself, exact in f32: two pieces hold a
-// bf16 number and six an f32 one, down to 2^-14 of the head's largest entry for
-// two pieces (2^-30 for six), below which the last piece's exponents end.
+// leaves a remainder of at most 2^-4 of itself, exact in f32, as long as it does
+// not run out of exponents at 2^-6: two pieces hold bf16 numbers down to 2^-14
+// of the head's largest entry, four down to 2^-22 and all to 2^-30 of it (queries
+// have columns far above the others, and the keys may make little of them); six
+// keep f32 numbers to 2^-38.  Four pieces of four heads are one MMA width, 16.
 // Probabilities (times the value scale): fixed point against the tile's largest,
 // 32 bits in eight digits of four (24 in six for the widest tile, whose O would
 // not fit TMEM otherwise).  The codes 0 .. 15 of e4m3 stand for 0 .. 15 times
@@ -396,7 +398,7 @@ template <typename T>
 struct Pieces;
 template <>
 struct Pieces<__nv_bfloat16> {
-  static constexpr int n = 2;
+  static constexpr int n = 4;
   using raw = uint2;  // four elements
   __device__ static __forceinline__ void open(uint2 w, float* v) {
     const float2 a = bf2_to_f2(w.x), b = bf2_to_f2(w.y);

@@ -238,6 +238,18 @@ def test_attention_over_unlike_scales(xkv):
     _check_attend(b, q, _attend(b, q))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_queries_with_a_column_that_the_keys_do_not_use(xkv, dt):
+    # one column 10^5 times the others, zero in the keys: what decides are entries at 2^-17 of the largest
+    b, g = _fill(xkv, 1, 1, 64, 16, 320, [300], dt)
+    b.c.k.view(torch.uint8)[..., 7] = 0
+    b.r["k"][..., 7] = 0.0
+    q = (2 * torch.randn((1, 8, 64), generator=g)).to(_dt(dt))
+    q[..., 7] = 1e5
+    q = q.cuda()
+    _check_attend(b, q, _attend(b, q))
+
+
 def test_attention_of_many_sequences(xkv):
     counts = [(37 * i) % 301 for i in range(700)]  # more sequences than CTAs, some empty
     b, g = _fill(xkv, 700, 1, 32, 16, 320, counts)
