@@ -518,7 +518,10 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ Walk s_walk;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
-  __shared__ float s_qc[kAhead][GQ], s_sum[2][2][4][GQ];
+  // factors of the logits of the last units: the queries run at most kAhead units before S, S kAhead tiles before P
+  constexpr int kFactors = 16;
+  static_assert(2 * kAhead + 2 <= kFactors, "factors kept");
+  __shared__ float s_qc[kFactors][GQ], s_sum[2][2][4][GQ];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sm;
   uint8_t* sv = sk + kStages * HDA * kAtom;
@@ -533,10 +536,10 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       mbar_init(&v_empty[lane], 1);
     }
     if (lane < kAhead) {
-      mbar_init(&s_full[lane], 1);
+      mbar_init(&s_full[lane], 2);
       mbar_init(&s_empty[lane], 4);
       mbar_init(&q_full[lane], 32);
-      mbar_init(&q_empty[lane], 1 + 256);
+      mbar_init(&q_empty[lane], 1);
     }
     if (lane < 2) {
       mbar_init(&p_full[lane], 128);
@@ -614,7 +617,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       if (g0 + q_head < a.gq && j < a.hd) raw[x] = *reinterpret_cast<const QRaw*>(q + j);
     }
   };
-  auto query_store = [&](const QRaw* raw, int g0, int qb) {
+  auto query_store = [&](const QRaw* raw, int g0, int seg) {
+    const int qb = seg % kAhead;
     float v[kQuads][4];
     uint32_t big = 0;
 #pragma unroll
@@ -632,7 +636,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
     const int e2 = scale_exp(big);
     const float inv = pow2f(-e2);
-    if ((lane & 7) == 0) s_qc[qb][g0 + q_head] = pow2f(e2) * q_scale;
+    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(e2) * q_scale;
 #pragma unroll
     for (int x = 0; x < kQuads; ++x)
 #pragma unroll
@@ -705,6 +709,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
               umma_e4m3(tmem + sb * Sh::ns, ka + (k / 4) * (kAtom >> 4) + (k % 4) * 2,
                         qa + (k / 4) * (Sh::ns * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
           umma_commit(&s_full[sb]);
+          mbar_arrive(&s_full[sb]);  // hands on the factors, which this warp saw with the queries
           umma_commit(&k_empty[st]);
           if (ends) umma_commit(&q_empty[qb]);
         }
@@ -781,7 +786,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) query_load(unit, g0 + 4 * k, raw[k]);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) query_store(raw[k], g0 + 4 * k, qb);
+            for (int k = 0; k < kBatch; ++k) query_store(raw[k], g0 + 4 * k, s1);
           }
           fence_proxy_async();
           mbar_arrive(&q_full[qb]);
@@ -862,22 +867,22 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         };
         scales(0, &ks, &vs);
         scales(1, &ks1, &vs1);
-        const int qb = seg % kAhead;
-        (void)wait(&q_full[qb], (seg / kAhead) & 1);
 #pragma unroll
         for (int g = 0; g < GQ; ++g) {
-          c[g] = s_qc[qb][g];
           l[g] = 0.f;
 #pragma unroll
           for (int x = 0; x < HDA; ++x) acc[x][g] = 0.f;
         }
         m = -INFINITY;
-        mbar_arrive(&q_empty[qb]);
         for (int i = first; i < i1; i += 2, at += 2 * kTile) {
           const int use = i >> 1, par = use & 1, sb = i % kAhead, t = t0 + i - i0;
           const bool live = at < len;
           (void)wait(&s_full[sb], (i / kAhead) & 1);
           tc_fence_after();
+          if (i == first) {
+#pragma unroll
+            for (int g = 0; g < GQ; ++g) c[g] = s_qc[seg % kFactors][g];
+          }
           float ks2 = 1.f, vs2 = 1.f;
           if (i + 4 < i1 && at + 4 * kTile < len) {
             ks2 = ksp[(at + 4 * kTile) >> lb];
