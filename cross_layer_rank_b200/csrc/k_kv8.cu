@@ -618,44 +618,46 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     }
   };
   auto query_store = [&](const QRaw* raw, int g0, int seg) {
-    const int qb = seg % kAhead;
     float v[kQuads][4];
     uint32_t big = 0;
 #pragma unroll
     for (int x = 0; x < kQuads; ++x) {
       Pieces<T>::open(raw[x], v[x]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t m = __float_as_uint(v[x][e]) & 0x7FFFFFFFu;
-        const bool finite = m < 0x7F800000u;
-        big = max(big, finite ? m : 0u);
-        v[x][e] = finite ? v[x][e] : __uint_as_float(0x7FC00000u);  // makes the head's logits NaN
-      }
+      for (int e = 0; e < 4; ++e) big = max(big, __float_as_uint(v[x][e]) & 0x7FFFFFFFu);
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
     const int e2 = scale_exp(big);
-    const float inv = pow2f(-e2);
-    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(e2) * q_scale;
+    // a head with an entry that is not finite has NaN logits
+    const float inv = big < 0x7F800000u ? pow2f(-e2) : __uint_as_float(0x7FC00000u);
+    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(min(e2, 120)) * q_scale;
 #pragma unroll
     for (int x = 0; x < kQuads; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[x][e] *= inv;
+    // row p * GQ + g0 + q_head, column 32 x + q_col: the swizzle's exclusive or splits into the lane's part and the
+    // step's, GQ being 4 or a multiple of 8 and g0 one of 4
+    const int row = g0 + q_head;
+    uint8_t* to = sq + (seg % kAhead) * HDA * Sh::ns * 128 + row * 128;
+    const uint32_t mine = swz128(row, q_col) - row * 128;
 #pragma unroll
     for (int p = 0; p < kNq; ++p)
 #pragma unroll
       for (int x = 0; x < kQuads; ++x) {
         float* r = v[x];
         const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
-        uint8_t* to = sq + (qb * HDA + x / 4) * Sh::ns * 128;
-        *reinterpret_cast<uint32_t*>(to + swz128(p * GQ + g0 + q_head, 32 * (x % 4) + q_col)) =
+        const uint32_t step = (2 * (x % 4) ^ ((p * GQ) & 7)) << 4;
+        *reinterpret_cast<uint32_t*>(to + (x / 4) * Sh::ns * 128 + p * GQ * 128 + (mine ^ step)) =
             c0 | static_cast<uint32_t>(c1) << 16;
         if (p + 1 < kNq) {
-          const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
-          r[0] = 16.f * (r[0] - f0.x);
-          r[1] = 16.f * (r[1] - f0.y);
-          r[2] = 16.f * (r[2] - f1.x);
-          r[3] = 16.f * (r[3] - f1.y);
+          const __half2 k16 = __half2half2(__ushort_as_half(0xCC00));  // -16: exact, 448 * 16 fits
+          const float2 f0 = __half22float2(__hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(c0, __NV_E4M3)), k16));
+          const float2 f1 = __half22float2(__hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3)), k16));
+          r[0] = fmaf(r[0], 16.f, f0.x);
+          r[1] = fmaf(r[1], 16.f, f0.y);
+          r[2] = fmaf(r[2], 16.f, f1.x);
+          r[3] = fmaf(r[3], 16.f, f1.y);
         }
       }
   };
