@@ -426,7 +426,7 @@ struct AttendShape {
   static constexpr int bytes_p = 2 * no * 128;
   static constexpr int cols(int ahead) { return ahead * ns + 2 * HDA * no; }
   static constexpr int stages_of(int ahead) {
-    const int s = (227 * 1024 - 8192 - 1024 - bytes_p - ahead * HDA * ns * 128) / (2 * HDA * kAtom);
+    const int s = (227 * 1024 - 9216 - 1024 - bytes_p - ahead * HDA * ns * 128) / (2 * HDA * kAtom);
     return s < kMaxStages ? s : kMaxStages;
   }
   // S runs up to `ahead` tiles before O, in as many buffers of TMEM and of the
@@ -912,13 +912,25 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           const float ev = static_cast<float>(static_cast<int>(vb >> 23) - 127 + (frac ? 1 : 0));
           const float vm = __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kDigitOne;
 #pragma unroll
-          for (int g = 0; g < GQ; ++g) {
-            s[g] = live ? s[g] : -INFINITY;  // times a positive factor
-            const float x = s[g] * (c[g] * ks);
-            const float x0 = redux_max(x), x1 = redux_max(x + ev);
-            if (lane == 0) {
-              s_max[wg][par][2 * g][quarter] = x0;
-              s_max[wg][par][2 * g + 1][quarter] = x1;
+          for (int g = 0; g < GQ; ++g) s[g] = live ? s[g] : -INFINITY;  // times a positive factor
+          if (lb >= 5) {  // a warp's rows share a scale, its first row's
+#pragma unroll
+            for (int g = 0; g < GQ; ++g) {
+              const float x0 = redux_max(s[g] * (c[g] * ks));
+              if (lane == 0) {
+                s_max[wg][par][2 * g][quarter] = x0;
+                s_max[wg][par][2 * g + 1][quarter] = x0 + ev;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < GQ; ++g) {
+              const float x = s[g] * (c[g] * ks);
+              const float x0 = redux_max(x), x1 = redux_max(x + ev);
+              if (lane == 0) {
+                s_max[wg][par][2 * g][quarter] = x0;
+                s_max[wg][par][2 * g + 1][quarter] = x1;
+              }
             }
           }
           named_bar_sync(1 + wg, 128);
