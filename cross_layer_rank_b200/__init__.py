@@ -6,7 +6,7 @@ There is no CPU or PyTorch fallback: importing this package fails loudly when
 libxkv.so has not been built (``python cross_layer_rank_b200/build.py``).
 
 Functions keep the C names (xkv_compress_group, xkv_build_landmarks,
-xkv_sr_attention_decode, xkv_full_reconstruct, xkv_ner, ...).  Tensors must be
+xkv_sr_attention_decode, xkv_full_reconstruct, xkv_ner, xkv_kv8_append, ...).  Tensors must be
 CUDA tensors, contiguous, of the dtype named by the call; errors raise
 XKVError carrying the library's status code.
 """

@@ -10,6 +10,8 @@
  *     online-softmax GQA attention over them plus a raw sink/recent window;
  *     and its xK-SR mode, where only the keys are compressed and the selected
  *     rows' values are read from the uncompressed cache.
+ * Beside them stands a whole cache in 8 bits: rows written into it, decode
+ * attention over it, and eviction of the blocks that attention used least.
  *
  * Sources (page title -- section):
  *   [xKV-blog] "xKV大模型压缩秘籍：跨层共享，小白也能轻松上手，收藏必备！" --
