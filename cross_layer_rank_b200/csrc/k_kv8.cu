@@ -604,15 +604,17 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   // A wait that runs out sets s_abort, after which no wait waits: the TMA and MMA
   // warps stop, the others run through their loops and meet every barrier.
   volatile int* abort = &s_abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (mbar_wait(bar, parity, a.status)) return true;
     *abort = 1;
     return false;
   };
+  // By a whole warp, which goes on together, and with one answer.
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
   const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
-  // By one warp, four query heads at a time, eight lanes to a head: their pieces into buffer qb, K-major rows
+  // By one warp, four query heads at a time, eight lanes to a head: their pieces into the unit's buffer, K-major rows
   // piece * GQ + g, zero past head_dim and past the group, and the factor of their logits.  A lane has four columns
   // of every 32; what it does is a chain of short steps, and these run side by side.
   using QRaw = typename Pieces<T>::raw;
@@ -680,11 +682,11 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           const int st = i % kStages;
           const uint32_t ph = ((i / kStages) & 1) ^ 1;
           const int unit = w.b * a.Hkv + w.h;
-          if (i >= kStages && !wait(&k_empty[st], ph)) break;
+          if (i >= kStages && !wait_one(&k_empty[st], ph)) break;
           mbar_arrive_expect_tx(&k_full[st], HDA * kAtom);
           for (int x = 0; x < HDA; ++x)
             tma_load_3d(sk + (st * HDA + x) * kAtom, &map_k, &k_full[st], 128 * x, w.t * kTile, unit);
-          if (i >= kStages && !wait(&v_empty[st], ph)) {
+          if (i >= kStages && !wait_one(&v_empty[st], ph)) {
             drain_ring(k_full, kStages, i + 1, a.status);
             drain_ring(v_full, kStages, i, a.status);
             i = -1;
