@@ -516,12 +516,17 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                      const AttendArgs a) {
   using Sh = AttendShape<T, GQ, HDA>;
   constexpr int kStages = Sh::stages, kAhead = Sh::ahead, kNq = Pieces<T>::n;
+  // Barriers of a full S.  A warpgroup waits for every other tile, and by parity: when it waits for tile i, the same
+  // barrier's use before must have ended.  Tile i - 2, its own, tells it that, with two barriers or more, S being in
+  // order; with one, tile i - 1 would still be running, and tile i - 2's phase be taken for tile i's.
+  constexpr int kFull = kAhead < 2 ? 2 : kAhead;
+  static_assert(kFull >= 2 && kFull % kAhead == 0, "barriers of S");
   constexpr int kDigits = digits<GQ, HDA>();
   constexpr float kDigitOne = kDigits == 8 ? 4294967296.f : 16777216.f;
   constexpr uint32_t kColO = kAhead * Sh::ns;  // O's first TMEM column, after the buffers of S
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  __shared__ __align__(8) uint64_t s_full[kAhead], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
+  __shared__ __align__(8) uint64_t s_full[kFull], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_tiles;
@@ -545,8 +550,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
       mbar_init(&v_full[lane], 1);
       mbar_init(&v_empty[lane], 1);
     }
+    if (lane < kFull) mbar_init(&s_full[lane], 2);
     if (lane < kAhead) {
-      mbar_init(&s_full[lane], 2);
       mbar_init(&s_empty[lane], 4);
       mbar_init(&q_full[lane], 32);
       mbar_init(&q_empty[lane], 1);
@@ -722,8 +727,8 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (k < ksteps)
               umma_e4m3(tmem + sb * Sh::ns, ka + (k / 4) * (kAtom >> 4) + (k % 4) * 2,
                         qa + (k / 4) * (Sh::ns * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
-          umma_commit(&s_full[sb]);
-          mbar_arrive(&s_full[sb]);  // hands on the factors, which this warp saw with the queries
+          umma_commit(&s_full[i % kFull]);
+          mbar_arrive(&s_full[i % kFull]);  // hands on the factors, which this warp saw with the queries
           umma_commit(&k_empty[st]);
           if (ends) umma_commit(&q_empty[qb]);
         }
@@ -891,7 +896,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         for (int i = first; i < i1; i += 2, at += 2 * kTile) {
           const int use = i >> 1, par = use & 1, sb = i % kAhead, t = t0 + i - i0;
           const bool live = at < len;
-          (void)wait(&s_full[sb], (i / kAhead) & 1);
+          (void)wait(&s_full[i % kFull], (i / kFull) & 1);
           tc_fence_after();
           if (i == first) {
 #pragma unroll

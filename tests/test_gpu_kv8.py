@@ -222,6 +222,24 @@ def test_attention_matches_float64(xkv, dt, H, gq, hd, block, counts):
     assert xkv.get_device_status() == 0
 
 
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("gq", [3, 8, 12])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_every_kernel_shape_over_shares_of_several_tiles(xkv, dt, gq, hd):
+    # 430 tiles on 148 SMs: each buffer of the pipeline is used again, by both halves of the softmax
+    b, g = _fill(xkv, 3, 2, hd, 32, 15040, [12000, 15001, 3], dt)
+    q = (2 * torch.randn((3, 2 * gq, hd), generator=g)).to(_dt(dt)).cuda()
+    b.c.weight.zero_()
+    out = _attend(b, q, accumulate=True)
+    assert xkv.get_device_status() == 0
+    _check_attend(b, q, out, np.zeros(b.c.weight.shape))
+    spoil = torch.empty(64 << 20, dtype=torch.int32, device="cuda")
+    for _ in range(8):  # codes from L2 and from memory, whose tiles come at other times
+        assert torch.equal(_attend(b, q), out)
+        spoil.zero_()
+    assert xkv.get_device_status() == 0
+
+
 def test_attention_over_unlike_scales(xkv):
     # blocks of values from 2^-60 to 2^60, keys from 2^-20 to 2^4, a peaked and a flat head
     b, g = _fill(xkv, 1, 2, 64, 8, 400, [389])
