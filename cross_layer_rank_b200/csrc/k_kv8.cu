@@ -1229,10 +1229,15 @@ struct EvictArgs {
   int64_t capacity;
   int Hkv, hd, block, budget, sink, recent;
   int ctas;  // of a unit's cluster
+  int keys;  // that shared memory has room for
+  int group;       // moves of a piece at most
+  uint32_t magic;  // v * magic >> 16 is v / vectors of a block, for v < 256 and blocks of up to 128
   int* status;
 };
 constexpr int kEvictCtas = 8;       // CTAs (one cluster) per unit at most; those of sequences within the budget leave at once
 constexpr int kEvictThreads = 256;
+constexpr int kEvictHeld = 8;         // keys that a thread holds in registers
+constexpr int64_t kEvictKeys = 16384;  // and a CTA in shared memory, three CTAs to an SM: past these they are read again
 constexpr int64_t kEvictMaxBlocks = 131072;  // three bit-mask arrays of a unit's blocks in shared memory
 
 // Order of a weight among the evictable blocks as an unsigned number: NaN below
@@ -1264,11 +1269,25 @@ __device__ inline int warp_scan(int n, int* out, F f) {
   return carry;
 }
 
-// Position of the r-th (from 0) set bit of `mask`, by a whole warp.
-__device__ __forceinline__ int nth_bit(uint32_t mask, int r) {
+// Position of the r-th (from 0) set bit of `mask`: one for a whole warp, or a
+// lane's own.
+__device__ __forceinline__ int nth_bit_warp(uint32_t mask, int r) {
   const int lane = threadIdx.x & 31;
   const bool is = ((mask >> lane) & 1u) && __popc(mask & ((1u << lane) - 1u)) == r;
   return __ffs(__ballot_sync(0xffffffffu, is)) - 1;
+}
+__device__ __forceinline__ int nth_bit(uint32_t mask, int r) {
+  int at = 0;
+#pragma unroll
+  for (int half = 16; half > 0; half >>= 1) {
+    const int c = __popc(mask & ((1u << half) - 1u));
+    if (r >= c) {
+      r -= c;
+      mask >>= half;
+      at += half;
+    }
+  }
+  return at;
 }
 
 // Last word whose prefix is <= r.
@@ -1283,14 +1302,19 @@ __device__ __forceinline__ int find_word(const int* pref, int lo, int hi, int r)
 
 // One cluster per unit.  Every CTA selects the `budget` blocks with the largest
 // keys itself (radix selection, eight bits a pass; up to 2048 keys stay in
-// registers), then the warps of the cluster move the kept blocks that stand past
-// the budget into the slots set free below it.  Slots read (>= budget - 1) and
-// written (< budget) meet only in slot budget - 1, which the last move writes:
-// the warp that moves a piece out of it moves the last block's piece in.
+// registers, up to 16384 in shared memory), then the warps of the cluster move
+// the kept blocks that stand past the budget into the slots set free below it.
+// Slots read (>= budget - 1) and written (< budget) meet only in slot budget - 1,
+// which the last move writes: the warp that moves a piece out of it moves the last
+// block's piece in.  kGroups: blocks of 2 KB at most, of which a warp moves several
+// at a time.
 // Four sequences cut from 16K to 8K tokens, 8 heads of 128 (35 MB to move), take
-// 19 us: 5 of selection, a chain of block-wide steps, 8 of moves (9 TB/s read and
-// written, the writes into L2) and the rest launch, loads and prefix sums.
-__global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArgs a) {
+// 18 us: 5 of selection, a chain of block-wide steps, 8 of moves (9 TB/s read and
+// written, the writes into L2) and the rest launch, loads and prefix sums.  Sixty
+// units cut from 5113 blocks of 8 x 48 to 2556 (59 MB to move) take 70 us, 178 with
+// one move at a time: the selection is 9 of them, for two rounds of CTAs.
+template <bool kGroups>
+__global__ void __launch_bounds__(kEvictThreads, 3) kv8_evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_dyn[];
   __shared__ uint32_t s_hist[2][256];
   __shared__ uint32_t s_prefix;
@@ -1309,25 +1333,39 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   const int64_t nblk = a.capacity / a.block;
   const float* weight = a.weight + unit * nblk;
   const int32_t* ids = a.ids + unit * nblk;
-  constexpr int kHeld = 8;  // keys a thread holds
-  const bool held = n <= kHeld * kEvictThreads;
+  constexpr int kHeld = kEvictHeld, kChunk = kHeld * kEvictThreads;
+  const bool held = n <= kChunk;
+  const int nw = (n + 31) / 32;
   const int last = ids[n - 1];
   auto key_of = [&](int i, float w, int id) {
     const bool safe = id < a.sink || static_cast<int64_t>(id) > static_cast<int64_t>(last) - a.recent || i == n - 1;
     return safe ? 0xFFFFFFFFu : weight_key(w);
   };
-  uint32_t mine[kHeld];
-  if (held) {
+  // keys of slots i, i + 256, ... (0 past the end), their loads in flight together
+  auto read = [&](int i, uint32_t* u) {
     float w[kHeld];
     int id[kHeld];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-      const int i = tid + k * kEvictThreads;
-      w[k] = i < n ? weight[i] : 0.f;
-      id[k] = i < n ? ids[i] : 0;
+      const bool in = i + k * kEvictThreads < n;
+      w[k] = in ? weight[i + k * kEvictThreads] : 0.f;
+      id[k] = in ? ids[i + k * kEvictThreads] : 0;
     }
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) mine[k] = key_of(tid + k * kEvictThreads, w[k], id[k]);
+    for (int k = 0; k < kHeld; ++k) u[k] = i + k * kEvictThreads < n ? key_of(i + k * kEvictThreads, w[k], id[k]) : 0u;
+  };
+  uint32_t mine[kHeld];
+  uint32_t* keys = s_dyn + 3 * nw;  // a thread reads only those that it wrote
+  const bool stored = !held && n <= a.keys;
+  if (held) {
+    read(tid, mine);
+  } else if (stored) {
+    for (int i = tid; i < n; i += kChunk) {
+      read(i, mine);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (i + k * kEvictThreads < n) keys[i + k * kEvictThreads] = mine[k];
+    }
   }
   // f(i, key) for the thread's slots, a warp's together
   auto each = [&](auto f) {
@@ -1336,9 +1374,16 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
       for (int k = 0; k < kHeld; ++k)
         if (k * kEvictThreads < n) f(tid + k * kEvictThreads, mine[k]);
     } else {
-      for (int base = 0; base < n; base += kEvictThreads) {
-        const int i = base + tid;
-        f(i, i < n ? key_of(i, weight[i], ids[i]) : 0u);
+      for (int base = 0; base < n; base += kChunk) {
+        if (stored) {
+#pragma unroll
+          for (int k = 0; k < kHeld; ++k) mine[k] = base + tid + k * kEvictThreads < n ? keys[base + tid + k * kEvictThreads] : 0u;
+        } else {
+          read(base + tid, mine);
+        }
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+          if (base + k * kEvictThreads < n) f(base + tid + k * kEvictThreads, mine[k]);
       }
     }
   };
@@ -1398,7 +1443,6 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   const uint32_t threshold = s_prefix;
   const int need = s_need;
   const bool whole = s_whole;
-  const int nw = (n + 31) / 32;
   uint32_t* keep = s_dyn;
   int* pref_m = reinterpret_cast<int*>(s_dyn + nw);
   uint32_t* equal = s_dyn + 2 * nw;
@@ -1444,38 +1488,71 @@ __global__ void __launch_bounds__(kEvictThreads) kv8_evict_kernel(const EvictArg
   // Moves r = 0 .. moves - 1, the last one (slot n - 1 to slot budget - 1) together with the first.
   const int moves = s_moves, rounds = max(moves - 1, 1);
   const bool pair = moves > 1;
-  auto place = [&](int r, int* src, int* dst) {
+  auto place = [&](int r, int* src, int* dst, auto nth) {
     const int wm = find_word(pref_m, 0, nw, r), wf = find_word(pref_f, 0, we + 1, r);
-    *src = wm * 32 + nth_bit(mover(wm), r - pref_m[wm]);
-    *dst = wf * 32 + nth_bit(empty(wf), r - pref_f[wf]);
+    *src = wm * 32 + nth(mover(wm), r - pref_m[wm]);
+    *dst = wf * 32 + nth(empty(wf), r - pref_f[wf]);
   };
-  // the codes in pieces of 32 x 8 vectors, dealt out to the cluster's warps, a piece's loads in flight together
+  // The codes in pieces of up to 32 x 8 vectors, dealt out to the cluster's warps, a piece's loads in flight together:
+  // of a block of more, a part; of smaller ones, as many moves as fit, but not so many that warps have none.  A lane
+  // finds its move's slots for the others, and takes the move's scale and weight (with K) or number (with V).
   const int nv = a.block * a.hd / 16, per = (nv + 255) / 256;  // vectors of a block, and pieces
   const int warps = a.ctas * kEvictThreads / 32, me = warp * a.ctas + rank;
+  const int group = !kGroups || 2 * rounds <= warps ? 1 : min(a.group, (2 * rounds + warps - 1) / warps);
+  const int pieces = (group == 1 ? rounds : (rounds + group - 1) / group) * 2 * per;
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int64_t w = me; w < static_cast<int64_t>(rounds) * 2 * per; w += warps) {
-    const int r = static_cast<int>(w / (2 * per)), q = static_cast<int>(w - static_cast<int64_t>(r) * 2 * per);
+  for (int w = me; w < pieces; w += warps) {
+    const int r0 = w / (2 * per) * group, q = w % (2 * per), m = min(group, rounds - r0);
     const int x = q >= per, first = (x ? q - per : q) * 256 + lane;
-    int src, dst;
-    place(r, &src, &dst);
-    uint4* rows = reinterpret_cast<uint4*>((x ? a.code[1] : a.code[0]) + unit * a.capacity * a.hd) + first;
-    // with a block's first piece go its scale and its weight (K) or number (V), by the first two lanes
-    uint32_t* tail = lane == 0 ? reinterpret_cast<uint32_t*>(x ? a.scale[1] : a.scale[0])
-                     : x       ? reinterpret_cast<uint32_t*>(a.ids)
-                               : reinterpret_cast<uint32_t*>(a.weight);
-    tail += unit * nblk;
-    const bool tails = (x ? q - per : q) == 0 && lane < 2;
+    int src = 0, dst = 0, left = m;  // moves of the piece
+    if (!kGroups || m == 1) place(r0, &src, &dst, nth_bit_warp);
+    else if (lane < m) place(r0 + lane, &src, &dst, nth_bit);
+    uint4* rows = reinterpret_cast<uint4*>((x ? a.code[1] : a.code[0]) + unit * a.capacity * a.hd);
+    uint32_t* scale = reinterpret_cast<uint32_t*>(x ? a.scale[1] : a.scale[0]) + unit * nblk;
+    uint32_t* other = (x ? reinterpret_cast<uint32_t*>(a.ids) : reinterpret_cast<uint32_t*>(a.weight)) + unit * nblk;
+    if (!kGroups && lane == 1) scale = other;  // two lanes for the one move
+    const bool tails = x ? q == per : q == 0;
+    bool again = r0 == 0 && pair;
     for (;;) {
       uint4 v[8];
-      const uint32_t t = tails ? tail[src] : 0u;
+      uint32_t t0 = 0u, t1 = 0u;
+      if (tails && lane < (kGroups ? left : 2)) {
+        t0 = scale[src];
+        if (kGroups) t1 = other[src];
+      }
+      if (!kGroups || left == 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (first + 32 * k < nv) v[k] = rows[static_cast<int64_t>(src) * nv + 32 * k];
+        for (int k = 0; k < 8; ++k)
+          if (first + 32 * k < nv) v[k] = rows[static_cast<int64_t>(src) * nv + first + 32 * k];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + 32 * k] = v[k];
-      if (tails) tail[dst] = t;
-      if (r > 0 || !pair || src == n - 1) break;
+        for (int k = 0; k < 8; ++k)
+          if (first + 32 * k < nv) rows[static_cast<int64_t>(dst) * nv + first + 32 * k] = v[k];
+      } else {  // blocks of 128 vectors at most: 32 bits number a unit's
+        auto vector = [&](int k, int slot, int* j) {
+          const int at = first + 32 * k;
+          *j = at * a.magic >> 16;
+          return __shfl_sync(0xffffffffu, slot, *j) * nv + at - *j * nv;
+        };
+        int j;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int from = vector(k, src, &j);
+          if (j < left) v[k] = rows[from];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int to = vector(k, dst, &j);
+          if (j < left) rows[to] = v[k];
+        }
+      }
+      if (tails && lane < (kGroups ? left : 2)) {
+        scale[dst] = t0;
+        if (kGroups) other[dst] = t1;
+      }
+      // the last move goes with the first one, thread by thread
+      if (!again) break;
+      again = false;
+      left = 1;
       src = n - 1;
       dst = edge;
     }
@@ -1670,18 +1747,26 @@ xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, con
   a.sink = sink;
   a.recent = recent;
   a.status = device_status_ptr();
-  const size_t smem = static_cast<size_t>((nblk + 31) / 32) * 3 * 4;
-  if (cudaFuncSetAttribute(kv8_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kEvictMaxBlocks / 32 * 3 * 4)) != cudaSuccess)
-    return XKV_ERR_CUDA;
-  // CTAs to a unit: up to eight, as long as each warp can get two pieces of the most blocks that can move.  A CTA of
-  // its own costs each the selection; with eight for every unit, 144 units of 9 blocks took 17 us, with one 6 us.
+  a.keys = nblk > kEvictHeld * kEvictThreads ? static_cast<int>(std::min(nblk, kEvictKeys)) : 0;
+  const size_t smem = static_cast<size_t>((nblk + 31) / 32) * 3 * 4 + static_cast<size_t>(a.keys) * 4;
+  const int nv = p->block * p->head_dim / 16;
+  a.group = nv > 128 ? 1 : std::min(256 / nv, 32);
+  a.magic = (65535u + nv) / nv;
+  // CTAs to a unit: up to eight, as long as each warp can get two pieces of the most blocks that can move, or, where
+  // SMs are idle, two moves.  A CTA of its own costs each the selection: with eight for every unit, 144 units of 9
+  // blocks took 17 us, with one 6 us; 60 units of 300 blocks (hd 48, 8 tokens each) cut to 150 take 16 us with eight
+  // and 12 with two, 2 units of 128 blocks 7.6 with one and 7.2 with four.
   const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(nblk - budget + 1, 1));
-  const int64_t pieces = 2 * moves * ((p->block * p->head_dim / 16 + 255) / 256);
+  const int64_t parts = 2 * moves * ((nv + 255) / 256), units = static_cast<int64_t>(p->batch) * p->n_kv_heads;
   a.ctas = 1;
-  while (a.ctas < kEvictCtas && pieces > 2 * a.ctas * (kEvictThreads / 32)) a.ctas *= 2;
-  return launch(kv8_evict_kernel, dim3(static_cast<unsigned>(p->batch) * p->n_kv_heads * a.ctas), kEvictThreads, smem, st,
-                a.ctas, a);
+  while (a.ctas < kEvictCtas && parts > 2 * a.ctas * (kEvictThreads / 32) *
+                                            (2 * a.ctas * units <= num_sms() ? 1 : a.group))
+    a.ctas *= 2;
+  auto* kernel = a.group > 1 ? kv8_evict_kernel<true> : kv8_evict_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kEvictMaxBlocks / 32 * 3 * 4 + kEvictKeys * 4)) != cudaSuccess)
+    return XKV_ERR_CUDA;
+  return launch(kernel, dim3(static_cast<unsigned>(units) * a.ctas), kEvictThreads, smem, st, a.ctas, a);
 }
 
 }  // namespace xkv

@@ -380,6 +380,8 @@ def _set_weight(b, w):
     (1, 1, 32, 8, [8 * 97], 32, 31, 1),     # and on its last
     (2, 2, 256, 128, [1280, 1281], 6, 1, 1),
     (1, 1, 16, 8, [8 * 5000 + 1], 1234, 5, 100),
+    (2, 1, 16, 8, [8 * 16384, 8 * 2049 - 7], 2000, 0, 1),  # the most keys that are kept, and the least that need room
+    (2, 1, 16, 8, [8 * 16384 + 1, 8 * 2048], 2047, 3, 5),  # past them
 ])
 def test_eviction_is_exact(xkv, B, H, hd, block, counts, budget, sink, recent):
     capacity = -(-max(counts) // block) * block + block
