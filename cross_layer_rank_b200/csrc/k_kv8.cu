@@ -1311,8 +1311,8 @@ __device__ __forceinline__ int find_word(const int* pref, int lo, int hi, int r)
 // Four sequences cut from 16K to 8K tokens, 8 heads of 128 (35 MB to move), take
 // 18 us: 5 of selection, a chain of block-wide steps, 8 of moves (9 TB/s read and
 // written, the writes into L2) and the rest launch, loads and prefix sums.  Sixty
-// units cut from 5113 blocks of 8 x 48 to 2556 (59 MB to move) take 70 us, 178 with
-// one move at a time: the selection is 9 of them, for two rounds of CTAs.
+// units cut from 5113 blocks of 8 x 48 to 2556 (59 MB to move) take 57 us, 178 with
+// one move at a time: the selection is 9 of them.
 template <bool kGroups>
 __global__ void __launch_bounds__(kEvictThreads, 3) kv8_evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_dyn[];
@@ -1755,11 +1755,14 @@ xkv_status kv8_evict_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, con
   // CTAs to a unit: up to eight, as long as each warp can get two pieces of the most blocks that can move, or, where
   // SMs are idle, two moves.  A CTA of its own costs each the selection: with eight for every unit, 144 units of 9
   // blocks took 17 us, with one 6 us; 60 units of 300 blocks (hd 48, 8 tokens each) cut to 150 take 16 us with eight
-  // and 12 with two, 2 units of 128 blocks 7.6 with one and 7.2 with four.
+  // and 11 with two, 2 units of 128 blocks 7.6 with one and 7.1 with four.  Small blocks, whose selection is most of the
+  // work, in one round of three CTAs an SM: 60 units of 5113 such blocks cut to 4758 30 us with four, 42 with eight.
+  // (With large blocks and ragged lengths the CTAs of sequences within the budget leave at once: 26 us with eight for
+  // 64 units, 40 with fewer.)
   const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(nblk - budget + 1, 1));
   const int64_t parts = 2 * moves * ((nv + 255) / 256), units = static_cast<int64_t>(p->batch) * p->n_kv_heads;
   a.ctas = 1;
-  while (a.ctas < kEvictCtas && parts > 2 * a.ctas * (kEvictThreads / 32) *
+  while (a.ctas < kEvictCtas && (a.group == 1 || 2 * a.ctas * units <= 3 * num_sms()) && parts > 2 * a.ctas * (kEvictThreads / 32) *
                                             (2 * a.ctas * units <= num_sms() ? 1 : a.group))
     a.ctas *= 2;
   auto* kernel = a.group > 1 ? kv8_evict_kernel<true> : kv8_evict_kernel<false>;
