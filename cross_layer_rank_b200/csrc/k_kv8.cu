@@ -270,7 +270,7 @@ struct Spot {
 };
 template <int N, typename F>
 __device__ inline int walk_line(const AttendArgs& a, Spot* spot, F targets) {
-  constexpr int kEach = 4;  // sequences a lane takes at a time
+  constexpr int kEach = 2;  // sequences a lane takes at a time
   const int lane = threadIdx.x & 31;
   int n[kEach], at = 0;  // the lane's sequences' places, and those before them
   auto load = [&](int base, int carry) {
