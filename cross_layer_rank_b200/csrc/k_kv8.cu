@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "xkv_common.cuh"
 #include "xkv_internal.h"
@@ -225,6 +226,7 @@ struct AttendArgs {
   int64_t capacity;
   int B, Hkv, gq, hd, block, tiles_cap;
   int ctas;
+  float q_scale;  // log2(e) / sqrt(hd)
   int* status;
 };
 
@@ -261,15 +263,15 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) { return (ro
 
 __device__ __forceinline__ int places_of(int nt) { return nt ? nt + 1 : 0; }
 
-// By one warp: N places of the line.  `targets` turns the line's length into
-// the places looked for, or -1 - b where the start of sequence b is.  A place is
+// By one warp: a place of the line.  `target` turns the line's length into the
+// place looked for, or -1 - b for the start of sequence b.  A place is
 // told as its sequence b, the places and the units that have rows before b; a
 // place past the end is at b = B.
 struct Spot {
   int b, before, units;
 };
-template <int N, typename F>
-__device__ inline int walk_line(const AttendArgs& a, Spot* spot, F targets) {
+template <typename F>
+__device__ inline int walk_line(const AttendArgs& a, Spot* spot, F target) {
   constexpr int kEach = 2;  // sequences a lane takes at a time
   const int lane = threadIdx.x & 31;
   int n[kEach], at = 0;  // the lane's sequences' places, and those before them
@@ -293,47 +295,34 @@ __device__ inline int walk_line(const AttendArgs& a, Spot* spot, F targets) {
   };
   int total = 0;
   for (int base = 0; base < a.B; base += 32 * kEach) total = load(base, total);
-  int x[N];
-  targets(total, x);
-  bool found[N];
-#pragma unroll
-  for (int t = 0; t < N; ++t) {
-    spot[t] = Spot{a.B, total, 0};
-    found[t] = false;
-  }
+  const int x = target(total);
+  *spot = Spot{a.B, total, 0};
   for (int base = 0, carry = 0; base < a.B; base += 32 * kEach) {
     if (a.B > 32 * kEach) carry = load(base, carry);  // else what was loaded still stands
-    unsigned some[kEach];  // lanes whose k-th sequence has rows
+    int hit_k = -1, hit_at = 0, p = at;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) some[k] = __ballot_sync(0xffffffffu, n[k] > 0);
-#pragma unroll
-    for (int t = 0; t < N; ++t) {
-      int hit_k = -1, hit_at = 0, p = at;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        if (x[t] >= 0 ? (x[t] >= p && x[t] < p + n[k]) : base + lane * kEach + k == -1 - x[t]) {
-          hit_k = k;
-          hit_at = p;
-        }
-        p += n[k];
+    for (int k = 0; k < kEach; ++k) {
+      if (x >= 0 ? (x >= p && x < p + n[k]) : base + lane * kEach + k == -1 - x) {
+        hit_k = k;
+        hit_at = p;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, hit_k >= 0);
-      int upto = 32 * kEach;  // of this round, the sequences before the place
-      if (hit && !found[t]) {
-        const int src = __ffs(hit) - 1;
-        upto = src * kEach + __shfl_sync(0xffffffffu, hit_k, src);
-        spot[t].b = base + upto;
-        spot[t].before = __shfl_sync(0xffffffffu, hit_at, src);
-      }
-      if (!found[t]) {
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const int lanes = (upto - k + kEach - 1) / kEach;
-          spot[t].units += a.Hkv * __popc(lanes >= 32 ? some[k] : some[k] & ((1u << lanes) - 1u));
-        }
-      }
-      found[t] |= hit != 0;
+      p += n[k];
     }
+    const unsigned hit = __ballot_sync(0xffffffffu, hit_k >= 0);
+    int upto = 32 * kEach;  // of this round, the sequences before the place
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      upto = src * kEach + __shfl_sync(0xffffffffu, hit_k, src);
+      spot->b = base + upto;
+      spot->before = __shfl_sync(0xffffffffu, hit_at, src);
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const unsigned some = __ballot_sync(0xffffffffu, n[k] > 0);  // lanes whose k-th sequence has rows
+      const int lanes = (upto - k + kEach - 1) / kEach;
+      spot->units += a.Hkv * __popc(lanes >= 32 ? some : some & ((1u << lanes) - 1u));
+    }
+    if (hit) break;
   }
   return total;
 }
@@ -529,7 +518,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   __shared__ __align__(8) uint64_t s_full[kFull], s_empty[kAhead], q_full[kAhead], q_empty[kAhead], p_full[2], o_full[2], done[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_tiles;
+  __shared__ int s_tiles[2];
   __shared__ Walk s_walk;
   __shared__ __align__(16) float s_max[2][2][2 * GQ][4];
   __shared__ __align__(16) float4 s_ref[2][2][4][GQ];
@@ -572,40 +561,43 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   let_next_start();  // not before: the joining kernel reads the lengths at once
   // nor TMEM, which an earlier kernel on this SM may still ask for while this one waits for it
   if (warp == kWarpS) tmem_alloc(&s_tmem, Sh::tmem);
-  if (warp == 0) {
-    Spot spot[2];
+  if (warp < 2) {  // the share's start by warp 0, its end by warp 1
+    Spot spot;
     Share share{0, 0};
-    walk_line<2>(a, spot, [&](int total, int* x) {
+    walk_line(a, &spot, [&](int total) {
       share = share_of(total, a.ctas, blockIdx.x);
-      x[0] = share.lo;
-      x[1] = share.hi;
+      return warp ? share.hi : share.lo;
     });
     if (lane == 0) {
-      int n = 0;
+      int ended = 0, places = 0;  // units that end before the place
       if (share.lo < share.hi) {
         Walk w;
-        w.b = spot[0].b;
-        w.load(a, rows_of(a, w.b));
-        w.h = (share.lo - spot[0].before) / (w.nt + 1);
-        w.t = share.lo - spot[0].before - w.h * (w.nt + 1);
-        // the share's tiles: its places less the empty one of every unit that ends in it
-        const int each = spot[1].b < a.B ? places_of(tiles_of(a, spot[1].b)) : 1;
-        n = share.hi - share.lo -
-            (spot[1].units + (share.hi - spot[1].before) / each - (spot[0].units + w.h));
-        if (n > 0 && w.t == w.nt) {  // the share starts with an empty place
-          w.t = w.nt - 1;
-          w.step(a);
+        w.b = spot.b;
+        if (warp == 0) {
+          w.load(a, rows_of(a, w.b));
+          w.h = (share.lo - spot.before) / (w.nt + 1);
+          w.t = share.lo - spot.before - w.h * (w.nt + 1);
+          ended = spot.units + w.h;
+          places = share.hi - share.lo;
+          if (w.t == w.nt && places > 1) {  // the share starts with an empty place
+            w.t = w.nt - 1;
+            w.step(a);
+          }
+          s_walk = w;
+        } else {
+          ended = spot.units;
+          if (spot.b < a.B) ended += (share.hi - spot.before) / places_of(tiles_of(a, spot.b));
         }
-        s_walk = w;
       }
-      s_tiles = n;
+      // the share's tiles: its places less the empty one of every unit that ends in it
+      s_tiles[warp] = places - (warp ? ended : -ended);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int n = s_tiles;
+  const int n = s_tiles[0] + s_tiles[1];
   // A wait that runs out sets s_abort, after which no wait waits: the TMA and MMA
   // warps stop, the others run through their loops and meet every barrier.
   volatile int* abort = &s_abort;
@@ -618,7 +610,6 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   };
   // By a whole warp, which goes on together, and with one answer.
   auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
-  const float q_scale = kLog2e / sqrtf(static_cast<float>(a.hd));
   // By one warp, four query heads at a time, eight lanes to a head: their pieces into the unit's buffer, K-major rows
   // piece * GQ + g, zero past head_dim and past the group, and the factor of their logits.  A lane has four columns
   // of every 32; what it does is a chain of short steps, and these run side by side.
@@ -648,7 +639,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int e2 = scale_exp(big);
     // a head with an entry that is not finite has NaN logits
     const float inv = big < 0x7F800000u ? pow2f(-e2) : __uint_as_float(0x7FC00000u);
-    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(min(e2, 120)) * q_scale;
+    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(min(e2, 120)) * a.q_scale;
 #pragma unroll
     for (int x = 0; x < kQuads; ++x)
 #pragma unroll
@@ -1068,7 +1059,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   // the lengths: the attention kernel lets this one start only when what came before it is done
   if (warp == 0) {
     Spot spot;
-    const int total = walk_line<1>(a, &spot, [&](int, int* x) { x[0] = -1 - b; });
+    const int total = walk_line(a, &spot, [&](int) { return -1 - b; });
     if (lane == 0) {
       s_before = spot.before;
       s_total = total;
@@ -1698,6 +1689,7 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
   a.block = p->block;
   a.tiles_cap = static_cast<int>(plan.tiles_cap);
   a.ctas = plan.ctas;
+  a.q_scale = kLog2e / std::sqrt(static_cast<float>(p->head_dim));
   a.status = device_status_ptr();
   CUtensorMap maps[2];
   for (int x = 0; x < 2; ++x) {
