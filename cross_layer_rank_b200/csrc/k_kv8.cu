@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "xkv_common.cuh"
 #include "xkv_internal.h"
@@ -610,53 +611,57 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   };
   // By a whole warp, which goes on together, and with one answer.
   auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
-  // By one warp, four query heads at a time, eight lanes to a head: their pieces into the unit's buffer, K-major rows
-  // piece * GQ + g, zero past head_dim and past the group, and the factor of their logits.  A lane has four columns
-  // of every 32; what it does is a chain of short steps, and these run side by side.
+  // By one warp, one, two or four query heads at a time, 32, 16 or 8 lanes to a head: their pieces into the unit's
+  // buffer, K-major rows piece * GQ + g, zero past head_dim and past the group, and the factor of their logits.  A lane
+  // has four columns of every 4 kLanes, kVecs times; what it does is a chain of short steps, and these run side by side.
   using QRaw = typename Pieces<T>::raw;
-  constexpr int kQuads = 4 * HDA;
-  const int q_head = lane >> 3, q_col = 4 * (lane & 7);
-  auto query_load = [&](int64_t unit, int g0, QRaw* raw) {
+  auto query_load = [&](int64_t unit, int g0, auto& raw) {
+    constexpr int kVecs = std::extent_v<std::remove_reference_t<decltype(raw)>>, kLanes = 32 * HDA / kVecs;
+    constexpr int kStep = 4 * kLanes;  // columns
+    const int q_head = lane / kLanes, q_col = 4 * (lane % kLanes);
     const T* q = static_cast<const T*>(a.q) + (unit * a.gq + g0 + q_head) * a.hd;
 #pragma unroll
-    for (int x = 0; x < kQuads; ++x) {
-      const int j = 32 * x + q_col;
+    for (int x = 0; x < kVecs; ++x) {
+      const int j = kStep * x + q_col;
       raw[x] = QRaw{};
       if (g0 + q_head < a.gq && j < a.hd) raw[x] = *reinterpret_cast<const QRaw*>(q + j);
     }
   };
-  auto query_store = [&](const QRaw* raw, int g0, int seg) {
-    float v[kQuads][4];
+  auto query_store = [&](const auto& raw, int g0, int seg) {
+    constexpr int kVecs = std::extent_v<std::remove_reference_t<decltype(raw)>>, kLanes = 32 * HDA / kVecs;
+    constexpr int kStep = 4 * kLanes;  // columns
+    const int q_head = lane / kLanes, q_col = 4 * (lane % kLanes);
+    float v[kVecs][4];
     uint32_t big = 0;
 #pragma unroll
-    for (int x = 0; x < kQuads; ++x) {
+    for (int x = 0; x < kVecs; ++x) {
       Pieces<T>::open(raw[x], v[x]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) big = max(big, __float_as_uint(v[x][e]) & 0x7FFFFFFFu);
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
     const int e2 = scale_exp(big);
     // a head with an entry that is not finite has NaN logits
     const float inv = big < 0x7F800000u ? pow2f(-e2) : __uint_as_float(0x7FC00000u);
-    if ((lane & 7) == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(min(e2, 120)) * a.q_scale;
+    if (lane % kLanes == 0) s_qc[seg % kFactors][g0 + q_head] = pow2f(min(e2, 120)) * a.q_scale;
 #pragma unroll
-    for (int x = 0; x < kQuads; ++x)
+    for (int x = 0; x < kVecs; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[x][e] *= inv;
-    // row p * GQ + g0 + q_head, column 32 x + q_col: the swizzle's exclusive or splits into the lane's part and the
-    // step's, GQ being 4 or a multiple of 8 and g0 one of 4
+    // row p * GQ + g0 + q_head, column kStep x + q_col: the swizzle's exclusive or splits into the lane's part and the
+    // step's, GQ being 4 or a multiple of 8
     const int row = g0 + q_head;
     uint8_t* to = sq + (seg % kAhead) * HDA * Sh::ns * 128 + row * 128;
     const uint32_t mine = swz128(row, q_col) - row * 128;
 #pragma unroll
     for (int p = 0; p < kNq; ++p)
 #pragma unroll
-      for (int x = 0; x < kQuads; ++x) {
+      for (int x = 0; x < kVecs; ++x) {
         float* r = v[x];
         const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
-        const uint32_t step = (2 * (x % 4) ^ ((p * GQ) & 7)) << 4;
-        *reinterpret_cast<uint32_t*>(to + (x / 4) * Sh::ns * 128 + p * GQ * 128 + (mine ^ step)) =
+        const uint32_t step = (kStep * x % 128 / 16 ^ ((p * GQ) & 7)) << 4;
+        *reinterpret_cast<uint32_t*>(to + (kStep * x / 128) * Sh::ns * 128 + p * GQ * 128 + (mine ^ step)) =
             c0 | static_cast<uint32_t>(c1) << 16;
         if (p + 1 < kNq) {
           const __half2 k16 = __half2half2(__ushort_as_half(0xCC00));  // -16: exact, 448 * 16 fits
@@ -771,6 +776,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     } else if (warp == kWarpQ) {
       // the queries of every unit after the first, as far ahead as there are buffers; the next unit's are loaded
       // (32 registers of them at most) while one is cut into pieces
+      constexpr int kQuads = 4 * HDA;  // eight lanes to a head
       constexpr int kMost = 128 / (kQuads * static_cast<int>(sizeof(QRaw)));
       constexpr int kBatch = kMost < GQ / 4 ? kMost : GQ / 4;
       QRaw raw[kBatch][kQuads], next[kBatch][kQuads];
@@ -808,11 +814,12 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           for (int x = 0; x < kQuads; ++x) raw[k][x] = next[k][x];
       }
     } else {
-      // the first unit's queries, which everything waits for, by a softmax warp for every four heads
-      if (warp < GQ / 4) {
-        QRaw raw[kQuads];
-        query_load(static_cast<int64_t>(w.b) * a.Hkv + w.h, 4 * warp, raw);
-        query_store(raw, 4 * warp, 0);
+      // the first unit's queries, which everything waits for, by a softmax warp for each head, or for every two
+      constexpr int kHeadsEach = GQ > 8 ? 2 : 1;
+      if (warp * kHeadsEach < GQ) {
+        QRaw raw[kHeadsEach * HDA];
+        query_load(static_cast<int64_t>(w.b) * a.Hkv + w.h, kHeadsEach * warp, raw);
+        query_store(raw, kHeadsEach * warp, 0);
       }
       fence_proxy_async();
       named_bar_sync(3, 256);
