@@ -222,6 +222,7 @@ struct AttendArgs {
   float2* ml;    // [slot][gq] their references and softmax sums
   float* wpart;  // [unit][tile][sub-block][gq] sums of the tile's weights, or NULL
   float* wref;   // [unit][tile][gq] the maxima they refer to
+  int2* span;    // [unit] the first and the last CTA whose share meets it, or NULL
   float* weight;
   float* out;
   int64_t capacity;
@@ -867,6 +868,10 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
         const int t0 = w.t, i1 = min(n, i0 + w.nt - t0);
         const int first = i0 + ((i0 ^ wg) & 1);
+        if (a.span && tid == 0) {
+          if (t0 == 0) a.span[unit].x = blockIdx.x;
+          if (t0 + i1 - i0 == w.nt) a.span[unit].y = blockIdx.x;
+        }
         const int len = w.len;
         const float* ksp = a.k_scale + unit * nblk;
         const float* vsp = a.v_scale + unit * nblk;
@@ -1064,20 +1069,33 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_start();
   // the lengths: the attention kernel lets this one start only when what came before it is done
-  if (warp == 0) {
-    Spot spot;
-    const int total = walk_line(a, &spot, [&](int) { return -1 - b; });
-    if (lane == 0) {
-      s_before = spot.before;
-      s_total = total;
-    }
-  }
   const int len = static_cast<int>(checked_len(a.lens[b], a.capacity, a.status));
   const int nt = (len + kTile - 1) / kTile;
-  __syncthreads();
-  const int x0 = s_before + h * (nt + 1);
-  const int c0 = nt ? cta_of(s_total, a.ctas, x0) : 0, c1 = nt ? cta_of(s_total, a.ctas, x0 + nt - 1) : 0;
+  // The CTAs whose shares meet the unit: found again while the attention runs, or, where its registers leave no room
+  // for this kernel beside it, as it wrote them.
+  int c0 = 0, c1 = 0;
+  if (!a.span) {
+    if (warp == 0) {
+      Spot spot;
+      const int total = walk_line(a, &spot, [&](int) { return -1 - b; });
+      if (lane == 0) {
+        s_before = spot.before;
+        s_total = total;
+      }
+    }
+    __syncthreads();
+    const int x0 = s_before + h * (nt + 1);
+    if (nt) {
+      c0 = cta_of(s_total, a.ctas, x0);
+      c1 = cta_of(s_total, a.ctas, x0 + nt - 1);
+    }
+  }
   wait_for_earlier();  // the attention's partials from here on
+  if (a.span && nt) {
+    const int2 c = a.span[unit];
+    c0 = c.x;
+    c1 = c.y;
+  }
   float* out = a.out + static_cast<int64_t>(unit) * gq * hd;
   if (nt == 0) {
     if (blockIdx.y == 0)
@@ -1645,7 +1663,8 @@ KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads) {
   r.off_ml = align_up(slots * gq * hd * 4);
   r.off_wpart = r.off_ml + align_up(slots * gq * 8);
   r.off_wref = r.off_wpart + align_up(static_cast<size_t>(units) * r.tiles_cap * spt * gq * 4);
-  r.bytes = r.off_wref + align_up(static_cast<size_t>(units) * r.tiles_cap * gq * 4);
+  r.off_span = r.off_wref + align_up(static_cast<size_t>(units) * r.tiles_cap * gq * 4);
+  r.bytes = r.off_span + align_up(static_cast<size_t>(units) * 8);
   return r;
 }
 
@@ -1687,6 +1706,8 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
     a.wref = reinterpret_cast<float*>(w + plan.off_wref);
     a.weight = c->weight;
   }
+  // 384 threads of 168 registers leave the joining kernel no room
+  if (n_q_heads / p->n_kv_heads > 4 || p->head_dim > 128) a.span = reinterpret_cast<int2*>(w + plan.off_span);
   a.out = out;
   a.capacity = p->capacity;
   a.B = p->batch;

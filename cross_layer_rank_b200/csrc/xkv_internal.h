@@ -103,7 +103,7 @@ xkv_status compress_launch(const CompressPlan& plan, const void* const* X, int G
 struct KV8Plan {
   int ctas;  // attention CTAs (shares of the tiles)
   int64_t tiles_cap;
-  size_t off_ml, off_wpart, off_wref, bytes;
+  size_t off_ml, off_wpart, off_wref, off_span, bytes;
 };
 KV8Plan kv8_plan(const xkv_kv8_params* p, int n_q_heads);
 xkv_status kv8_append_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, const int32_t* lens,
