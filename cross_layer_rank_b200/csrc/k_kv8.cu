@@ -222,7 +222,7 @@ struct AttendArgs {
   float2* ml;    // [slot][gq] their references and softmax sums
   float* wpart;  // [unit][tile][sub-block][gq] sums of the tile's weights, or NULL
   float* wref;   // [unit][tile][gq] the maxima they refer to
-  int2* span;    // [unit] the first and the last CTA whose share meets it, or NULL
+  int2* span;    // [unit] the first and the last CTA whose share meets it
   float* weight;
   float* out;
   int64_t capacity;
@@ -250,13 +250,6 @@ __device__ __forceinline__ Share share_of(int total, int n, int c) {
   s.hi = s.lo + q + (c < r ? 1 : 0);
   return s;
 }
-// The CTA whose share holds tile x.
-__device__ __forceinline__ int cta_of(int total, int n, int x) {
-  const int q = total / n, r = total % n;
-  const int cut = r * (q + 1);
-  return x < cut ? x / (q + 1) : r + (x - cut) / q;
-}
-
 // Rows of sequence b, within the cache (the joining kernel records a length outside), and their tiles.
 __device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {
   return min(max(a.lens[b], 0), static_cast<int>(a.capacity));
@@ -266,9 +259,8 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) { return (ro
 __device__ __forceinline__ int places_of(int nt) { return nt ? nt + 1 : 0; }
 
 // By one warp: a place of the line.  `target` turns the line's length into the
-// place looked for, or -1 - b for the start of sequence b.  A place is
-// told as its sequence b, the places and the units that have rows before b; a
-// place past the end is at b = B.
+// place looked for.  A place is told as its sequence b, the places and the units
+// that have rows before b; a place past the end is at b = B.
 struct Spot {
   int b, before, units;
 };
@@ -304,7 +296,7 @@ __device__ inline int walk_line(const AttendArgs& a, Spot* spot, F target) {
     int hit_k = -1, hit_at = 0, p = at;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      if (x >= 0 ? (x >= p && x < p + n[k]) : base + lane * kEach + k == -1 - x) {
+      if (x >= p && x < p + n[k]) {
         hit_k = k;
         hit_at = p;
       }
@@ -868,7 +860,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const int64_t unit = static_cast<int64_t>(w.b) * a.Hkv + w.h;
         const int t0 = w.t, i1 = min(n, i0 + w.nt - t0);
         const int first = i0 + ((i0 ^ wg) & 1);
-        if (a.span && tid == 0) {
+        if (tid == 0) {
           if (t0 == 0) a.span[unit].x = blockIdx.x;
           if (t0 + i1 - i0 == w.nt) a.span[unit].y = blockIdx.x;
         }
@@ -1053,45 +1045,28 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 // a warp by slot; CTAs (unit, y >= head_ctas) add a share of the blocks' weights,
 // sum_g 2^(ref - M_g) wpart / L_g.  What it costs is latency, so every thread has
 // its loads in flight together, one CTA takes several heads where there are
-// units enough, and the launch is a programmatic one: its CTAs find their unit
-// while the attention still runs.  About 2.5 us after the attention's end for two
+// units enough, and the launch is a programmatic one.  Which CTAs met the unit is
+// read as the attention wrote it: found again from the lengths, while the attention
+// ran, it cost 1.1 us for 8 heads, beside whose 168 registers a thread these CTAs find no
+// room before the attention's end (one-tile units: 10.7 -> 9.6 us).  About 2.5 us after the attention's end for two
 // sequences of 128K tokens (38 slots to each of 8 x 7 heads, 1024 blocks).
 constexpr int kCombineThreads = 256;
 constexpr int kMaxSlots = 2 * 256;      // of one unit: two for each CTA
 constexpr int kWeightBlocks = 64;       // blocks whose weights a CTA has in hand at a time
 
 __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const AttendArgs a, int heads, int head_ctas) {
-  __shared__ int s_before, s_total;
   __shared__ float s_f[8][kMaxSlots];
   __shared__ float s_m[16], s_r[16];
   __shared__ __align__(16) float s_red[8][256];
-  const int unit = blockIdx.x, b = unit / a.Hkv, h = unit % a.Hkv, gq = a.gq, hd = a.hd;
+  const int unit = blockIdx.x, b = unit / a.Hkv, gq = a.gq, hd = a.hd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_start();
   // the lengths: the attention kernel lets this one start only when what came before it is done
   const int len = static_cast<int>(checked_len(a.lens[b], a.capacity, a.status));
   const int nt = (len + kTile - 1) / kTile;
-  // The CTAs whose shares meet the unit: found again while the attention runs, or, where its registers leave no room
-  // for this kernel beside it, as it wrote them.
-  int c0 = 0, c1 = 0;
-  if (!a.span) {
-    if (warp == 0) {
-      Spot spot;
-      const int total = walk_line(a, &spot, [&](int) { return -1 - b; });
-      if (lane == 0) {
-        s_before = spot.before;
-        s_total = total;
-      }
-    }
-    __syncthreads();
-    const int x0 = s_before + h * (nt + 1);
-    if (nt) {
-      c0 = cta_of(s_total, a.ctas, x0);
-      c1 = cta_of(s_total, a.ctas, x0 + nt - 1);
-    }
-  }
-  wait_for_earlier();  // the attention's partials from here on
-  if (a.span && nt) {
+  wait_for_earlier();  // what the attention wrote from here on
+  int c0 = 0, c1 = 0;  // the CTAs whose shares met the unit
+  if (nt) {
     const int2 c = a.span[unit];
     c0 = c.x;
     c1 = c.y;
@@ -1706,8 +1681,7 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
     a.wref = reinterpret_cast<float*>(w + plan.off_wref);
     a.weight = c->weight;
   }
-  // 384 threads of 168 registers leave the joining kernel no room
-  if (n_q_heads / p->n_kv_heads > 4 || p->head_dim > 128) a.span = reinterpret_cast<int2*>(w + plan.off_span);
+  a.span = reinterpret_cast<int2*>(w + plan.off_span);
   a.out = out;
   a.capacity = p->capacity;
   a.B = p->batch;
