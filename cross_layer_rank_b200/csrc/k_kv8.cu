@@ -491,8 +491,8 @@ __device__ __forceinline__ void group_sums(const float* p, int sub, F f) {
 // read once: 537.3 MB of DRAM reads; the tensor pipe is 8 % busy).  Otherwise by
 // the chain of a tile's steps, about 2500 clocks with 8 query heads, of which two
 // warpgroups have one each in flight: 48 sequences of 1 to 8192 tokens, 4 x 8 heads
-// of 64, take 25 us (23 MB).  Three warpgroups (512 threads, registers moved to
-// them) spilled: 72 us instead of 54 for two sequences of 128K tokens, 4 x 7 heads.
+// of 64, take 23 us (23 MB).  Three warpgroups (512 threads, registers moved to
+// them) spilled: 72 us instead of 53 for two sequences of 128K tokens, 4 x 7 heads.
 template <typename T, int GQ, int HDA>
 __global__ void __launch_bounds__(kAttendThreads, 1)
 kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -1558,7 +1558,8 @@ __global__ void __launch_bounds__(kEvictThreads, 3) kv8_evict_kernel(const Evict
 // earlier one may have written or read (the joining kernel's lengths apart, see
 // there), and lets the next one start its own preparation: launched
 // programmatically, the calls of a decode step hide each other's launch and set-up
-// (append of one token 2.6 -> 2.3 us, a short attention 10.4 -> 9.9).
+// (append of one token 2.6 -> 2.3 us, a short attention 10.4 -> 9.9; the latter is 8.9
+// since its start was shortened).
 template <typename... P, typename... A>
 static xkv_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
                          const A&... args) {
