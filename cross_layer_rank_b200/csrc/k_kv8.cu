@@ -1104,7 +1104,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
       for (int e = 0; e < kHeld; ++e) {
         // a slot without rows has l = 0; m = M = -inf where all of a unit's logits are NaN
         const float w = l[e] == 0.f ? 0.f : m[e] == M ? 1.f : exp2f(m[e] - M);
-        if (w != 0.f) L += l[e] * w;
+        L = fmaf(l[e], w, L);  // 0 * NaN too: a slot whose every logit is NaN refers to -inf
         const int k = from + 32 * e + lane;
         if (f && k < slots) f[k] = slots <= 32 * kHeld ? w : l[e] == 0.f ? NAN : m[e];
       }

@@ -295,6 +295,33 @@ def test_nan_reaches_only_its_own_heads(xkv):
     assert torch.equal(out, good)
 
 
+@pytest.mark.parametrize("gq,hd,block,counts,unit,rows", [
+    (4, 64, 16, [129, 40], (0, 1), (128, 129)),         # a tile's only row
+    (2, 128, 64, [512, 512], (1, 0), (128, 256)),       # a whole tile beside finite ones
+    (16, 256, 32, [300, 129], (1, 0), (128, 129)),
+    (8, 64, 32, [40000, 1], (0, 0), (25600, 25728)),    # one of more slots than a lane holds
+    (4, 128, 128, [60000], (0, 1), (59904, 60000)),     # the last tile
+    (4, 64, 16, [300], (0, 0), (0, 300)),               # every row
+])
+def test_nan_keys_with_a_tile_of_their_own(xkv, gq, hd, block, counts, unit, rows):
+    # all logits of a partial are NaN, and those of the others are not: the softmax's sum is NaN all the same
+    capacity = -(-max(counts) // block) * block + block
+    b, g = _fill(xkv, len(counts), 2, hd, block, capacity, counts)
+    q = torch.randn((len(counts), 2 * gq, hd), generator=g).to(torch.bfloat16).cuda()
+    b.c.weight.zero_()
+    good = _attend(b, q, accumulate=True)
+    weight = b.c.weight.clone()
+    b.c.weight.zero_()
+    s, h = unit
+    b.c.k.view(torch.uint8)[s, h, rows[0]:rows[1], 3] = 0x7F
+    out = _attend(b, q, accumulate=True)
+    live = -(-counts[s] // block)
+    assert out[s, h * gq:(h + 1) * gq].isnan().all() and b.c.weight[s, h, :live].isnan().all()
+    out[s, h * gq:(h + 1) * gq], b.c.weight[s, h, :live] = good[s, h * gq:(h + 1) * gq], weight[s, h, :live]
+    assert torch.equal(out, good) and torch.equal(b.c.weight, weight)
+    assert xkv.get_device_status() == 0
+
+
 def test_attention_writes_only_its_outputs(xkv):
     counts = [77, 0, 300]
     b, g = _fill(xkv, 3, 2, 80, 16, 304, counts)
