@@ -1080,7 +1080,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
   // the unit's slots: two for each CTA whose share meets it
   const int sf = gq * hd, slots = 2 * (c1 - c0 + 1);
   const float* base = a.part + 2 * static_cast<int64_t>(unit + c0) * sf;
-  // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M)
+  // by one warp: head g's largest reference M and 1 / L, and (where `f` is one) every slot's 2^(m - M), NaN for a slot
+  // without rows
   auto head = [&](int g, float* f) {
     constexpr int kHeld = 2;  // slots a lane holds: 64 in all, the rest in further rounds
     const float2* ml = a.ml + 2 * static_cast<int64_t>(unit + c0) * gq + g;  // below 2^31 from here on: 512 slots
@@ -1106,11 +1107,12 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
         const float w = l[e] == 0.f ? 0.f : m[e] == M ? 1.f : exp2f(m[e] - M);
         L = fmaf(l[e], w, L);  // 0 * NaN too: a slot whose every logit is NaN refers to -inf
         const int k = from + 32 * e + lane;
-        if (f && k < slots) f[k] = slots <= 32 * kHeld ? w : l[e] == 0.f ? NAN : m[e];
+        if (f && k < slots) f[k] = l[e] == 0.f ? NAN : slots <= 32 * kHeld ? w : m[e];
       }
     }
     if (f && slots > 32 * kHeld)  // M has moved since: from the references again
-      for (int k = lane; k < slots; k += 32) f[k] = isnan(f[k]) ? 0.f : f[k] == M ? 1.f : exp2f(f[k] - M);
+      for (int k = lane; k < slots; k += 32)
+        if (!isnan(f[k])) f[k] = f[k] == M ? 1.f : exp2f(f[k] - M);
     L = warp_sum(L);
     if (lane == 0) {
       s_m[g] = M;
@@ -1151,8 +1153,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
           const int k = from + j * wph;
-          const float f = k < slots ? s_f[slot][k] : 0.f;
-          if (f == 0.f) continue;  // a slot without rows holds anything
+          const float f = k < slots ? s_f[slot][k] : NAN;
+          if (isnan(f)) continue;  // a slot without rows holds anything; one of factor 0 may hold a NaN
           add(x, f, v[j]);
           if (hi) add(y, f, z[j]);
         }

@@ -322,6 +322,24 @@ def test_nan_keys_with_a_tile_of_their_own(xkv, gq, hd, block, counts, unit, row
     assert xkv.get_device_status() == 0
 
 
+@pytest.mark.parametrize("gq,hd,block,n,row", [(4, 64, 16, 300, 130), (16, 256, 32, 200, 128), (2, 128, 64, 60000, 30000),
+                                              (8, 64, 8, 129, 128)])
+def test_nan_values_of_rows_without_weight(xkv, gq, hd, block, n, row):
+    # logits of 800 for the first rows and 0 for the others, whose probabilities are 0 in f32: 0 * NaN stays NaN,
+    # whichever partial has the row
+    b, g = _fill(xkv, 1, 2, hd, block, -(-n // block) * block, [n])
+    b.c.k.view(torch.uint8).zero_()
+    b.c.k[:, :, :8] = torch.full((1, 2, 8, hd), 8.0).to(F8).cuda()
+    b.c.k_scale.fill_(1.0)
+    q = torch.full((1, 2 * gq, hd), 100.0 / hd ** 0.5, dtype=torch.float32, device="cuda")
+    good = _attend(b, q)
+    b.c.v.view(torch.uint8)[0, 1, row, 9] = 0x7F
+    out = _attend(b, q)
+    assert out[0, gq:, 9].isnan().all()
+    out[0, gq:, 9] = good[0, gq:, 9]
+    assert torch.equal(out, good)
+
+
 def test_attention_writes_only_its_outputs(xkv):
     counts = [77, 0, 300]
     b, g = _fill(xkv, 3, 2, 80, 16, 304, counts)
