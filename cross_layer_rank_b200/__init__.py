@@ -12,6 +12,7 @@ XKVError carrying the library's status code.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Optional, Sequence
@@ -211,6 +212,25 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _pool_of(stream, device):
+    """Context in which torch allocates from the pool of the stream that a call runs on.  What a call allocates itself
+    has to come from there: memory of the current stream's pool may still be used by earlier work on that stream, and
+    goes to later work on it while the call runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # 0 and 1 both name the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call, which others may have once the call has returned."""
+    with _pool_of(stream, device):
+        return workspace(nbytes, device)
+
+
 def _wsize(fn, *args) -> int:
     n = C.c_size_t(0)
     _check(fn(*args, C.byref(n)), fn.__name__)
@@ -235,7 +255,8 @@ def xkv_gram_accumulate(layers: Sequence[torch.Tensor], C_out: torch.Tensor, ws:
     ldx = layers[0].stride(0)
     ptrs = (C.c_void_p * G)(*[t.data_ptr() for t in layers])
     nbytes = xkv_gram_workspace_size(G, rows, d, layers[0].dtype)
-    ws = ws if ws is not None else workspace(nbytes, layers[0].device)
+    if ws is None:
+        ws = _scratch(nbytes, layers[0].device, stream)
     _check(lib.xkv_gram_accumulate(ptrs, G, rows, d, ldx, dtype_code(layers[0].dtype), _ptr(C_out), _ptr(ws),
                                    ws.numel(), _stream(stream)), "xkv_gram_accumulate")
 
@@ -258,7 +279,8 @@ def xkv_compress_group(layers: Sequence[torch.Tensor], rank: int, A: torch.Tenso
             raise ValueError("layers must share shape and row stride")
     dt = dtype_code(layers[0].dtype)
     nbytes = xkv_compress_workspace_size(G, T, d, rank, oversample, shard_rows, layers[0].dtype)
-    ws = ws if ws is not None else workspace(nbytes, layers[0].device)
+    if ws is None:
+        ws = _scratch(nbytes, layers[0].device, stream)
     ptrs = (C.c_void_p * G)(*[t.data_ptr() for t in layers])
     _check(lib.xkv_compress_group(ptrs, G, T, d, ldx, dt, rank, iters, oversample, shard_rows, seed, _ptr(A),
                                   _ptr(Bt), _ptr(eigvals), _ptr(gram_out), _ptr(ws), ws.numel(), _stream(stream)),
@@ -274,7 +296,8 @@ def xkv_factor_gram(gram: torch.Tensor, G: int, d: int, rows: int, rank: int, Bt
                     eigvals: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
     """Top-r basis of a given (G d)^2 f32 Gram: Bt (G d x rank, Bt's dtype), optional f32 V_r and Ritz values."""
     nbytes = xkv_factor_workspace_size(G, d, rows, rank, oversample, Bt.dtype)
-    ws = ws if ws is not None else workspace(nbytes, gram.device)
+    if ws is None:
+        ws = _scratch(nbytes, gram.device, stream)
     _check(lib.xkv_factor_gram(_ptr(gram), G, d, rows, dtype_code(Bt.dtype), rank, iters, oversample, seed, _ptr(Bt),
                                _ptr(Vr_out), _ptr(eigvals), _ptr(ws), ws.numel(), _stream(stream)), "xkv_factor_gram")
 
@@ -295,7 +318,8 @@ def xkv_project(layers: Sequence[torch.Tensor], V: torch.Tensor, A: torch.Tensor
     rank = V.shape[1]
     if A.shape[-1] != rank or A.stride(-1) != 1 or not A.is_cuda:
         raise ValueError("A must be T x rank with contiguous rows")
-    ws = ws if ws is not None else workspace(xkv_project_workspace_size(G, d, rank), layers[0].device)
+    if ws is None:
+        ws = _scratch(xkv_project_workspace_size(G, d, rank), layers[0].device, stream)
     ptrs = (C.c_void_p * G)(*[t.data_ptr() for t in layers])
     _check(lib.xkv_project(ptrs, G, T, d, ldx, dtype_code(layers[0].dtype), _ptr(V), dtype_code(V.dtype), rank,
                            C.c_void_p(A.data_ptr()), A.stride(0), _ptr(ws), ws.numel(), _stream(stream)),
@@ -349,7 +373,8 @@ def xkv_sr_attention_decode(p: SRParams, q, A_K, Bt_K, A_V, Bt_V, landmarks, sr_
                             sel_out=None, ws=None, stream=None):
     """One SR decode step of one layer; writes out [B][Hq][hd] f32 (and sel_out).
     A, Bt, landmarks and windows may be views: their strides come from p."""
-    ws = ws if ws is not None else workspace(xkv_sr_workspace_size(p), q.device)
+    if ws is None:
+        ws = _scratch(xkv_sr_workspace_size(p), q.device, stream)
     _check(lib.xkv_sr_attention_decode(C.byref(p), _ptr(q), _addr(A_K), _addr(Bt_K), _addr(A_V), _addr(Bt_V),
                                        _addr(landmarks), _addr(sr_K), _addr(sr_V), _ptr(out), _ptr(sel_out),
                                        _ptr(ws), ws.numel(), _stream(stream)), "xkv_sr_attention_decode")
@@ -389,7 +414,8 @@ def xkv_xk_sr_attention_decode_host_values(p: SRParams, q, A_K, Bt_K, V_host: to
     only the kept chunks' rows are read over the host link."""
     if V_host.is_cuda or not V_host.is_pinned():
         raise ValueError("V_host must be a pinned host tensor")
-    ws = ws if ws is not None else workspace(xkv_xk_sr_host_workspace_size(p), q.device)
+    if ws is None:
+        ws = _scratch(xkv_xk_sr_host_workspace_size(p), q.device, stream)
     _check(lib.xkv_xk_sr_attention_decode_host_values(C.byref(p), _ptr(q), _addr(A_K), _addr(Bt_K),
                                                       C.c_void_p(V_host.data_ptr()), _addr(landmarks), _addr(sr_K),
                                                       _addr(sr_V), _ptr(out), _ptr(sel_out), _ptr(ws), ws.numel(),
@@ -404,7 +430,8 @@ def xkv_xk_sr_attention_decode(p: SRParams, q, A_K, Bt_K, V, landmarks, sr_K, sr
                                stream=None):
     """One xK-SR decode step of one layer (values read from the uncompressed V
     [B][T][d]); writes out [B][Hq][hd] f32 (and sel_out)."""
-    ws = ws if ws is not None else workspace(xkv_xk_sr_workspace_size(p), q.device)
+    if ws is None:
+        ws = _scratch(xkv_xk_sr_workspace_size(p), q.device, stream)
     _check(lib.xkv_xk_sr_attention_decode(C.byref(p), _ptr(q), _ptr(A_K), _ptr(Bt_K), _ptr(V), _ptr(landmarks),
                                           _ptr(sr_K), _ptr(sr_V), _ptr(out), _ptr(sel_out), _ptr(ws), ws.numel(),
                                           _stream(stream)), "xkv_xk_sr_attention_decode")
@@ -447,7 +474,8 @@ def xkv_dense_workspace_size(p: DenseParams) -> int:
 
 
 def xkv_dense_attention_decode(p: DenseParams, q, K, V, out, ws=None, stream=None):
-    ws = ws if ws is not None else workspace(xkv_dense_workspace_size(p), q.device)
+    if ws is None:
+        ws = _scratch(xkv_dense_workspace_size(p), q.device, stream)
     _check(lib.xkv_dense_attention_decode(C.byref(p), _ptr(q), _ptr(K), _ptr(V), _ptr(out), _ptr(ws), ws.numel(),
                                           _stream(stream)), "xkv_dense_attention_decode")
 
@@ -541,9 +569,9 @@ def xkv_kv8_attention_decode(p: KV8Params, cache: KV8Cache, lens, q, out, accumu
                              stream=None):
     """One decode step over the 8-bit cache; writes out [B][Hq][hd] f32 and, with accumulate, adds
     every block's attention weight to cache.weight."""
+    raw = _kv8_check(p, cache, stream, lens, q, out, lens if ws is None else ws)
     if ws is None:
-        ws = workspace(xkv_kv8_workspace_size(p, q.shape[1] if q.dim() == 3 else 0), q.device)
-    stream = _kv8_check(p, cache, stream, lens, q, out, ws)
+        ws = _scratch(xkv_kv8_workspace_size(p, q.shape[1] if q.dim() == 3 else 0), q.device, stream)
     shape = q.shape
     if len(shape) != 3 or shape[0] != p.batch or shape[2] != p.head_dim or out.shape != shape or \
             out.dtype != torch.float32:
@@ -552,7 +580,7 @@ def xkv_kv8_attention_decode(p: KV8Params, cache: KV8Cache, lens, q, out, accumu
         raise ValueError("expected contiguous tensors")
     _check(lib.xkv_kv8_attention_decode(p, cache.pointers, _lens_ptr(p, lens), shape[1], dtype_code(q.dtype),
                                         q.data_ptr(), out.data_ptr(), 1 if accumulate else 0, ws.data_ptr(),
-                                        ws.numel() * ws.element_size(), stream), "xkv_kv8_attention_decode")
+                                        ws.numel() * ws.element_size(), raw), "xkv_kv8_attention_decode")
 
 
 def xkv_kv8_evict(p: KV8Params, cache: KV8Cache, lens, budget: int, sink: int, recent: int, lens_out, stream=None):
@@ -571,7 +599,8 @@ def xkv_ner_workspace_size(n: int, block: int) -> int:
 def xkv_ner(gram: torch.Tensor, block: int, ner_out, erank_out=None, rank_out=None, rank_rel_tol: float = 1e-9,
             ws=None, stream=None):
     n = gram.shape[0]
-    ws = ws if ws is not None else workspace(xkv_ner_workspace_size(n, block), gram.device)
+    if ws is None:
+        ws = _scratch(xkv_ner_workspace_size(n, block), gram.device, stream)
     _check(lib.xkv_ner(_ptr(gram), n, block, rank_rel_tol, _ptr(ner_out), _ptr(erank_out), _ptr(rank_out), _ptr(ws),
                        ws.numel(), _stream(stream)), "xkv_ner")
 
@@ -581,8 +610,11 @@ def xkv_energy_rank(gram, block: int, energy: float = 0.95, rank_out=None, lambd
     total, and optionally its eigenvalues in descending order."""
     n = gram.shape[0]
     count = n // block
-    rank_out = rank_out if rank_out is not None else torch.empty(count, dtype=torch.int32, device=gram.device)
-    ws = ws if ws is not None else workspace(xkv_ner_workspace_size(n, block), gram.device)
+    if rank_out is None:
+        with _pool_of(stream, gram.device):
+            rank_out = torch.empty(count, dtype=torch.int32, device=gram.device)
+    if ws is None:
+        ws = _scratch(xkv_ner_workspace_size(n, block), gram.device, stream)
     _check(lib.xkv_energy_rank(_ptr(gram), n, block, float(energy), _ptr(rank_out), _ptr(lambda_out), _ptr(ws),
                                ws.numel(), _stream(stream)), "xkv_energy_rank")
     return rank_out
@@ -611,7 +643,8 @@ def xkv_sr_append(p: AppendParams, k_new, v_new, win_K, win_V, Bt_K, Bt_V, A_K, 
     arr = lambda ts: (C.c_void_p * G)(*[t.data_ptr() for t in ts])
     n = C.c_size_t(0)
     _check(lib.xkv_sr_append_workspace_size(C.byref(p), C.byref(n)), "xkv_sr_append_workspace_size")
-    ws = ws if ws is not None else workspace(n.value, A_K.device)
+    if ws is None:
+        ws = _scratch(n.value, A_K.device, stream)
     rolled = C.c_int(0)
     _check(lib.xkv_sr_append(C.byref(p), arr(k_new), arr(v_new), arr(win_K), arr(win_V), _ptr(Bt_K), _ptr(Bt_V),
                              _ptr(A_K), _ptr(A_V), arr(landmarks), C.byref(rolled), _ptr(ws), ws.numel(),
@@ -640,7 +673,7 @@ def xkv_sr_attention_partial(p: SRParams, shard: ShardParams, sel, q, A_K, Bt_K,
     if ws is None:
         n = C.c_size_t(0)
         _check(lib.xkv_sr_partial_workspace_size(C.byref(p), C.byref(n)), "xkv_sr_partial_workspace_size")
-        ws = workspace(n.value, q.device)
+        ws = _scratch(n.value, q.device, stream)
     _check(lib.xkv_sr_attention_partial(C.byref(p), C.byref(shard), _ptr(sel), _ptr(q), _addr(A_K), _addr(Bt_K),
                                         _addr(A_V), _addr(Bt_V), _addr(sr_K), _addr(sr_V), _ptr(out), _ptr(ml_out),
                                         _ptr(ws), ws.numel(), _stream(stream)), "xkv_sr_attention_partial")

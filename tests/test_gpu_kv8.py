@@ -546,6 +546,32 @@ def test_graphs_streams_and_a_shared_workspace(xkv):
     assert xkv.get_device_status() == 0
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_another_stream_takes_its_workspace_there(xkv, raw):
+    # the call's own workspace goes back when the call returns, long before it has run: what the current stream
+    # allocates meanwhile is other memory
+    b, g = _fill(xkv, 2, 2, 128, 64, 4096, [4000, 333])
+    q = torch.randn((2, 8, 128), generator=g).to(torch.bfloat16).cuda()
+    want, lens = _attend(b, q), b.dev_lens()
+    out = torch.full_like(want, float("nan"))
+    n = xkv.xkv_kv8_workspace_size(b.p, 8)
+    s, x = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    torch.empty(n, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(s):
+        torch.empty(n, dtype=torch.uint8, device="cuda")
+        x = torch.clamp(x @ x, -1, 1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            x = torch.clamp(x @ x, -1, 1)
+    xkv.xkv_kv8_attention_decode(b.p, b.c, lens, q, out, stream=s.cuda_stream if raw else s)
+    for _ in range(200):
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    assert not s.query()  # the call was still to run
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and xkv.get_device_status() == 0
+
+
 def _chain(xkv, seed, steps, wait):
     """Steps of append, attention with weights and eviction, one behind the other; every output and the last cache."""
     B, H, gq, hd, block, budget = 5, 2, 8, 64, 16, 9
