@@ -488,9 +488,24 @@ def kv8_params(batch, n_kv_heads, head_dim, block, capacity) -> KV8Params:
 class KV8Cache:
     """One layer's 8-bit KV cache: k, v [B][Hkv][capacity][hd] float8_e4m3fn, k_scale, v_scale
     [B][Hkv][capacity / block] f32 and, for eviction, weight (f32) and ids (int32) of the same
-    shape as the scales.  The tensors stay the caller's; the object keeps them alive."""
+    shape as the scales.  The tensors stay the caller's; the object keeps them alive.  One may be replaced
+    by another of its size (cache.k = cache.k[order]), and the next call takes that one; sizes stay, and so
+    does each tensor's memory while it is part of the cache (no resize_, set_ or assignment to .data)."""
+
+    TENSORS = ("k", "v", "k_scale", "v_scale", "weight", "ids")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None, ids=None):
+        self._take(k, v, k_scale, v_scale, weight, ids)
+
+    def __setattr__(self, name, value):
+        if name not in self.TENSORS:
+            return object.__setattr__(self, name, value)
+        held = {x: getattr(self, x) for x in self.TENSORS}
+        if name in ("k", "v") and value.shape != held[name].shape:
+            raise ValueError("a cache keeps its sizes: make a new KV8Cache")
+        self._take(**{**held, name: value})
+
+    def _take(self, k, v, k_scale, v_scale, weight, ids):
         for t, dt in ((k, torch.float8_e4m3fn), (v, torch.float8_e4m3fn), (k_scale, torch.float32),
                       (v_scale, torch.float32), (weight, torch.float32), (ids, torch.int32)):
             if t is None:
@@ -505,10 +520,13 @@ class KV8Cache:
         for t in (v_scale, weight, ids):
             if t is not None and t.shape != k_scale.shape:
                 raise ValueError("scales, weight and ids need one shape")
-        self.k, self.v, self.k_scale, self.v_scale, self.weight, self.ids = k, v, k_scale, v_scale, weight, ids
+        tensors = (k, v, k_scale, v_scale, weight, ids)
+        # a new object each time: a copy of this cache may share the old one
+        pointers = KV8Pointers(*(_ptr(t) for t in tensors))
+        self.__dict__.update(zip(self.TENSORS, tensors))
         self.index = k.get_device()
         self.sizes = (*k.shape, k.shape[2] // k_scale.shape[2])
-        self.pointers = KV8Pointers(*(_ptr(t) for t in (k, v, k_scale, v_scale, weight, ids)))
+        self.pointers = pointers
 
     @classmethod
     def empty(cls, p: KV8Params, device=None):

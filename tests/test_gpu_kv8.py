@@ -611,6 +611,24 @@ def test_calls_behind_one_another_and_side_by_side(xkv):
     assert xkv.get_device_status() == 0
 
 
+def test_a_replaced_tensor_is_read_and_written(xkv):
+    # sequences in another order, and weights started anew
+    b, g = _fill(xkv, 3, 2, 64, 16, 256, [200, 0, 77])
+    q = torch.randn((3, 8, 64), generator=g).to(torch.bfloat16).cuda()
+    b.c.weight.zero_()
+    want, weight = _attend(b, q, accumulate=True), b.c.weight.clone()
+    order = torch.tensor([2, 0, 1], device="cuda")
+    old = b.c.weight
+    for x in ("k", "v"):
+        setattr(b.c, x, getattr(b.c, x).view(torch.uint8)[order].view(F8))
+    for x in ("k_scale", "v_scale", "ids"):
+        setattr(b.c, x, getattr(b.c, x)[order])
+    b.c.weight = torch.zeros_like(old)
+    b.lens = [b.lens[i] for i in order.tolist()]
+    assert torch.equal(_attend(b, q[order], accumulate=True), want[order])
+    assert torch.equal(b.c.weight, weight[order]) and torch.equal(old, weight)
+
+
 def test_binding_refuses_what_the_library_cannot_see(xkv):
     b, g = _fill(xkv, 2, 2, 64, 16, 64, [10, 20])
     q, out = torch.zeros((2, 4, 64), device="cuda"), torch.empty((2, 4, 64), device="cuda")

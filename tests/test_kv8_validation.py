@@ -106,3 +106,29 @@ def test_binding_checks_the_cache_tensors(xkv):
                 (k, k, s.double(), s), (k, k, s, s, None, torch.zeros(nblk)), (k, k, torch.ones((2, 2, 15)), s)):
         with pytest.raises(ValueError):
             xkv.KV8Cache(*bad)
+
+
+def test_replaced_tensors_are_the_ones_that_calls_take(xkv, monkeypatch):
+    import copy
+    monkeypatch.setattr(xkv, "_ptr", lambda t: None if t is None else t.data_ptr())  # host tensors will do here
+    f8, rows, nblk = torch.float8_e4m3fn, (2, 2, 256, 64), (2, 2, 16)
+    new = {"k": lambda: torch.zeros(rows, dtype=torch.uint8).view(f8), "v": lambda: torch.zeros(rows, dtype=torch.uint8).view(f8),
+           "k_scale": lambda: torch.ones(nblk), "v_scale": lambda: torch.ones(nblk), "weight": lambda: torch.zeros(nblk),
+           "ids": lambda: torch.zeros(nblk, dtype=torch.int32)}
+    c = xkv.KV8Cache(**{x: f() for x, f in new.items()})
+    other = copy.copy(c)
+    before = {x: getattr(c.pointers, x) for x in new}
+    for x, f in new.items():
+        t = f()
+        setattr(c, x, t)
+        assert getattr(c, x) is t and getattr(c.pointers, x) == t.data_ptr() != before[x]
+        assert getattr(other.pointers, x) == before[x] == getattr(other, x).data_ptr()
+    c.weight = None
+    assert c.weight is None and c.pointers.weight is None and c.pointers.ids == c.ids.data_ptr()
+    held = {x: getattr(c.pointers, x) for x in new}
+    for x, bad in (("k", c.k[:1]), ("k", c.k.view(torch.uint8)), ("v", c.v[..., :32]), ("k_scale", c.k_scale[..., :8]),
+                   ("v_scale", c.v_scale.double()), ("ids", torch.zeros(nblk)), ("weight", c.k_scale[:1])):
+        kept = getattr(c, x)
+        with pytest.raises(ValueError):
+            setattr(c, x, bad)
+        assert getattr(c, x) is kept and {y: getattr(c.pointers, y) for y in new} == held
