@@ -366,19 +366,32 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) {
 // have columns far above the others, and the keys may make little of them); six
 // keep f32 numbers to 2^-38.  Four pieces of four heads are one MMA width, 16.
 // Probabilities (times the value scale): fixed point against the tile's largest,
-// 32 bits in eight digits of four (24 in six for the widest tile, whose O would
-// not fit TMEM otherwise).  The codes 0 .. 15 of e4m3 stand for 0 .. 15 times
-// 2^-9 (its subnormals and first binade), so a digit is its own code.
+// 32 bits in eight digits of four.  The codes 0 .. 15 of e4m3 stand for 0 .. 15
+// times 2^-9 (its subnormals and first binade), so a digit is its own code.  The
+// widest tile, whose O of eight columns a head would not fit TMEM, has six pieces
+// as the queries have: all 24 bits of a product down to 2^-14 of the tile's largest
+// and the rest to 2^-38 of it, where six digits would end at 2^-24 (an attention
+// sink, or one large value of a block, leaves the other rows of a tile that far
+// below).  They cost the conversions there and back.
 template <int GQ, int HDA>
 __host__ __device__ constexpr int digits() { return GQ * HDA == 32 ? 6 : 8; }
 
-// Four digits as four bytes: of byte i of a and byte j of b (with six digits,
-// a and b are below 2^24).
-template <int D>
-__device__ __forceinline__ uint32_t spread(uint32_t a, int i, uint32_t b, int j) {
-  const uint32_t y = D == 8 ? __byte_perm(a, 0u, 0x4040u | i | j << 8)  // one number's bytes i, j
-                            : __byte_perm(a, b, 0x7430u | i | j << 8);
+// Four digits as four bytes: of bytes i and j of a.
+__device__ __forceinline__ uint32_t spread(uint32_t a, int i, int j) {
+  const uint32_t y = __byte_perm(a, 0u, 0x4040u | i | j << 8);
   return (y | y << 4) & 0x0F0F0F0Fu;
+}
+
+// The next piece of two numbers as two codes, and what is left of them times 16.
+__device__ __forceinline__ uint32_t next_piece(float& a, float& b, bool last) {
+  const uint16_t c = to_e4m3x2(a, b);
+  if (!last) {
+    const __half2 k16 = __half2half2(__ushort_as_half(0xCC00));  // -16: exact, 448 * 16 fits
+    const float2 f = __half22float2(__hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)), k16));
+    a = fmaf(a, 16.f, f.x);
+    b = fmaf(b, 16.f, f.y);
+  }
+  return c;
 }
 template <typename T>
 struct Pieces;
@@ -505,7 +518,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
   constexpr int kFull = kAhead < 2 ? 2 : kAhead;
   static_assert(kFull >= 2 && kFull % kAhead == 0, "barriers of S");
   constexpr int kDigits = digits<GQ, HDA>();
-  constexpr float kDigitOne = kDigits == 8 ? 4294967296.f : 16777216.f;
+  constexpr float kUnit = kDigits == 8 ? 4294967296.f : 256.f;  // the digits', or the first piece's, of a tile's 1
   constexpr uint32_t kColO = kAhead * Sh::ns;  // O's first TMEM column, after the buffers of S
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
@@ -652,19 +665,9 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #pragma unroll
       for (int x = 0; x < kVecs; ++x) {
         float* r = v[x];
-        const uint16_t c0 = to_e4m3x2(r[0], r[1]), c1 = to_e4m3x2(r[2], r[3]);
+        const uint32_t c0 = next_piece(r[0], r[1], p + 1 == kNq), c1 = next_piece(r[2], r[3], p + 1 == kNq);
         const uint32_t step = (kStep * x % 128 / 16 ^ ((p * GQ) & 7)) << 4;
-        *reinterpret_cast<uint32_t*>(to + (kStep * x / 128) * Sh::ns * 128 + p * GQ * 128 + (mine ^ step)) =
-            c0 | static_cast<uint32_t>(c1) << 16;
-        if (p + 1 < kNq) {
-          const __half2 k16 = __half2half2(__ushort_as_half(0xCC00));  // -16: exact, 448 * 16 fits
-          const float2 f0 = __half22float2(__hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(c0, __NV_E4M3)), k16));
-          const float2 f1 = __half22float2(__hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3)), k16));
-          r[0] = fmaf(r[0], 16.f, f0.x);
-          r[1] = fmaf(r[1], 16.f, f0.y);
-          r[2] = fmaf(r[2], 16.f, f1.x);
-          r[3] = fmaf(r[3], 16.f, f1.y);
-        }
+        *reinterpret_cast<uint32_t*>(to + (kStep * x / 128) * Sh::ns * 128 + p * GQ * 128 + (mine ^ step)) = c0 | c1 << 16;
       }
   };
   if (n > 0) {
@@ -922,7 +925,7 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
           // O: references are whole numbers, so that every change of one is an exact power of two.
           const uint32_t vb = __float_as_uint(vs), frac = vb & 0x7FFFFFu;  // vs = vm 2^ev, vm in (1/2, 1]
           const float ev = static_cast<float>(static_cast<int>(vb >> 23) - 127 + (frac ? 1 : 0));
-          const float vm = __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kDigitOne;
+          const float vm = __uint_as_float(frac | (frac ? 0x3F000000u : 0x3F800000u)) * kUnit;
 #pragma unroll
           for (int g = 0; g < GQ; ++g) s[g] = live ? s[g] : -INFINITY;  // times a positive factor
           if (lb >= 5) {  // a warp's rows share a scale, its first row's
@@ -953,34 +956,58 @@ kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             const float mn = fmaxf(m, ceilf(fmaxf(fmaxf(x0.x, x0.y), fmaxf(x0.z, x0.w))));
             const float mv = ceilf(fmaxf(fmaxf(x1.x, x1.y), fmaxf(x1.z, x1.w)));
             const float al = m == mn ? 1.f : pow2_whole(m - mn);
-            // O's digits are 2^-9 of what they stand for, its sum is in units of the highest, 1 is 16 of those
-            ref[lane] = make_float4(mn, mv, al, ex2(mv - mn) * (512.f / 16.f));
+            // O's digits are 2^-9 of what they stand for, its sum is in units of the highest, 1 is 16 of those; of
+            // pieces, it is in units of the first
+            ref[lane] = make_float4(mn, mv, al, ex2(mv - mn) * (kDigits == 8 ? 512.f / 16.f : 1.f / kUnit));
             m = mn;
           }
           if (use > 0 && i > first) fold(use - 1);
           __syncwarp();
-          float p[GQ];
-          uint32_t fix[GQ];
+          float p[GQ], pv[GQ];
 #pragma unroll
           for (int g = 0; g < GQ; ++g) {
             const float4 r = ref[g];
             const float ck = c[g] * ks;
             p[g] = ex2(fmaf(s[g], ck, -r.x));
             l[g] = fmaf(l[g], r.z, p[g]);
-            // a NaN is 0 here, and the sum l has it; 1 itself is the largest number below it
-            fix[g] = __float2uint_rn(ex2(fmaf(s[g], ck, ev - r.y)) * vm);
-            if (kDigits < 8) fix[g] = min(fix[g], (1u << (4 * (kDigits & 7))) - 1u);
+            pv[g] = ex2(fmaf(s[g], ck, ev - r.y)) * vm;
           }
-#pragma unroll
-          for (int k = 0; k < Sh::no / 16; ++k) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int m = 8 * k + 2 * e, n1 = m + 1;  // the word's bytes in the row of numbers
-              o[e] = spread<kDigits>(fix[m / (kDigits / 2)], m % (kDigits / 2), fix[n1 / (kDigits / 2)], n1 % (kDigits / 2));
-            }
+          auto put = [&](int k, const uint32_t* o) {  // sixteen columns of this token's row
             *reinterpret_cast<uint4*>(p_row + (k / 2) * kTile * 32 + (((k & 1) * 16) ^ p_flip)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
+          };
+          if constexpr (kDigits == 8) {
+#pragma unroll
+            for (int k = 0; k < Sh::no / 16; ++k) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // a NaN is 0 here, and the sum l has it; 1 itself is the largest number below it
+                const uint32_t fix = __float2uint_rn(pv[2 * k + e / 2]);
+                o[e] = spread(fix, 2 * (e & 1), 2 * (e & 1) + 1);
+              }
+              put(k, o);
+            }
+          } else {
+            // the last piece first, as the digits' lowest: twelve bytes of two heads, 48 of eight
+#pragma unroll
+            for (int g0 = 0; g0 < GQ; g0 += 8) {
+              uint32_t o[12];
+#pragma unroll
+              for (int g = 0; g < 8; g += 2) {
+                uint32_t c2[3];  // two pieces of both heads, from the first ones
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                  const uint32_t a0 = next_piece(pv[g0 + g], pv[g0 + g + 1], false);
+                  c2[x] = a0 << 16 | next_piece(pv[g0 + g], pv[g0 + g + 1], x == 2);
+                }
+                o[g / 2 * 3] = __byte_perm(c2[2], c2[1], 0x6420);
+                o[g / 2 * 3 + 1] = __byte_perm(c2[0], c2[2], 0x7520);
+                o[g / 2 * 3 + 2] = __byte_perm(c2[1], c2[0], 0x7531);
+              }
+#pragma unroll
+              for (int k = 0; k < 3; ++k) put(g0 / 8 * 3 + k, o + 4 * k);
+            }
           }
           if (len - t * kTile < kTile) {
             const int st = i % kStages;

@@ -256,6 +256,56 @@ def test_attention_over_unlike_scales(xkv):
     _check_attend(b, q, _attend(b, q))
 
 
+def _tight(b, q, top):
+    """_bounds with the probabilities' own precision: what a product of probability and scale loses, beside the f32
+    share, is against the largest of its 128-row tile, of which the unit is less than twice: 2^-32 of the unit in 32
+    bits (rounding, or 1 to the number below it); in six pieces of four significant bits 2^-38 of it below 2^-14 of it
+    (half of the last piece's least code, 2^-10 16^-5 where the unit is 2^8), and above that 2^-24 of the product
+    itself, which is one more half-ulp of the f32 share."""
+    gq = q.shape[1] // b.r["k"].shape[1]
+    six = gq > 8 and q.shape[2] > 128
+    a = dict(b.r)
+    a["v"] = np.abs(b.r["v"])
+    tol = 2.0 ** -24 * (8 * top + 65) * ref.attend(a, b.block, b.lens, q)[0]
+    for i, n in enumerate(b.lens):
+        at = np.arange(n) // b.block
+        for h in range(b.r["k"].shape[1] if n else 0):
+            k = b.r["k"][i, h, :n] * b.r["k_scale"][i, h, at][:, None]
+            s = q[i, h * gq:(h + 1) * gq] @ k.T / np.sqrt(q.shape[2])
+            p = np.exp(s - s.max(1, keepdims=True))
+            p *= b.r["v_scale"][i, h, at] / p.sum(1, keepdims=True)
+            for t in range(0, n, 128):
+                most = p[:, t:t + 128].max(1)
+                tol[i, h * gq:(h + 1) * gq] += 2.0 ** (-37 if six else -31) * most[:, None] * a["v"][i, h, t:min(t + 128, n)].sum(0)
+    return tol
+
+
+@pytest.mark.parametrize("kind", ["outlier", "sink", "both"])
+@pytest.mark.parametrize("dt,gq,hd,block", [("bf16", 16, 256, 8), ("f32", 16, 256, 8), ("bf16", 9, 144, 16),
+                                            ("bf16", 8, 256, 8), ("bf16", 16, 128, 8), ("f32", 3, 64, 8)])
+def test_rows_that_weigh_little_beside_their_tile(xkv, kind, dt, gq, hd, block):
+    # an outlier value 2^13 times the others makes its block's scale large; a sink has nearly all of the probability
+    # and no value.  What the other rows of the tile bring is the whole of most columns, and as exact as ever.
+    n = 300
+    g = torch.Generator().manual_seed(11)
+    b = Both(xkv, 1, 1, hd, block, 320)
+    k, v = torch.randn((1, n, 1, hd), generator=g) * 0.1, torch.randn((1, n, 1, hd), generator=g)
+    u = torch.sign(torch.randn(hd, generator=g))
+    q = u * 0.25 + 0.25 * torch.randn((1, gq, hd), generator=g)
+    if kind != "outlier":
+        k[0, 5, 0] = u * 48 / hd ** 0.5  # a logit of about 12
+        v[0, 5] = 0.0
+    if kind != "sink":
+        v[0, 43, 0, 7] = 2.0 ** 13
+    b.append(k.to(_dt(dt)).cuda(), v.to(_dt(dt)).cuda())
+    q = q.to(_dt(dt)).cuda()
+    out = _attend(b, q)
+    qd = q.double().cpu().numpy()
+    want, _, top = ref.attend(b.r, block, b.lens, qd)
+    err, tol = np.abs(out.double().cpu().numpy() - want), _tight(b, qd, top)
+    assert top < 40 and (err <= tol).all(), float((err / tol).max())
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_queries_with_a_column_that_the_keys_do_not_use(xkv, dt):
     # one column 10^5 times the others, zero in the keys: what decides are entries at 2^-17 of the largest
