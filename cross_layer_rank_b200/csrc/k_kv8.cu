@@ -169,9 +169,13 @@ __global__ void __launch_bounds__(append_threads(W)) kv8_append_kernel(const App
   } else {
     __syncwarp();  // every lane has read the old scale
   }
-  const float now = fmaxf(was, pow2f(scale_exp(big)));
-  if (started && now > was) {
-    // the block's scale grows: its codes once more, on the new scale
+  // The block's own scale, raised to a power of two (a block written by other means may have any), 2^120 at most; a NaN
+  // leaves it to the rows.
+  const uint32_t wb = __float_as_uint(was) & 0x7FFFFFFFu;
+  const float least = wb > 0x7F800000u ? 0.f : fminf(__uint_as_float((wb + 0x7FFFFFu) & 0x7F800000u), pow2f(120));
+  const float now = fmaxf(least, pow2f(scale_exp(big)));
+  if (started && now != was) {
+    // another scale than the block had: its codes once more, on the new one
     const float ratio = was / now;
     uint4* old = reinterpret_cast<uint4*>(a.code[kv] + (unit * a.capacity + lo) * a.hd);
     for (int v = tid; v < static_cast<int>(len - lo) * vpr; v += nthr) {

@@ -467,7 +467,10 @@ typedef struct xkv_kv8_cache {
  * infinite value becomes the largest code, a NaN stays NaN, and neither counts
  * for the scale.  A block that held rows before keeps the larger of its scale
  * and the new rows' one; when that makes its scale grow, its codes are rounded
- * once more on the new scale.  A block opened by the call gets weight 0 and the
+ * once more on the new scale.  A scale of the block that is no power of two (a
+ * cache filled by other means; attention takes any positive scale) is raised to
+ * the next one in the same way, and one above 2^120 becomes 2^120.  A block
+ * opened by the call gets weight 0 and the
  * number after the last block's.  Rows past the capacity are dropped and
  * XKV_ERR_INVALID_ARG is recorded in the device status word.  lens is not
  * advanced. */

@@ -160,6 +160,37 @@ def test_append_special_values(xkv):
     assert b.r["k_scale"][0, 0, 0] == b.r["k_scale"][0, 0, 5] == 2.0 ** -117
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("mantissa", [1.0, 1.25, 1.5, 1.75])
+def test_append_to_a_block_with_a_scale_of_other_origin(xkv, dt, mantissa):
+    # blocks written by another quantiser, their scales no powers of two: what joins them is on the next power, and so
+    # are their own codes (times mantissa / 2, which e4m3's four bits times three leave exact in f32)
+    B, H, hd, block, held = 2, 2, 64, 16, 21
+    b, g = _fill(xkv, B, H, hd, block, 64, [held, held], dt)
+    for x in ("k", "v"):
+        getattr(b.c, x + "_scale")[:, :, 1].mul_(mantissa)
+        b.r[x + "_scale"][:, :, 1] *= mantissa
+    before = {x: b.r[x].copy() for x in ("k", "v")}
+    new = {x: _rows(g, B, 3, H, hd, dt, 0.25) for x in ("k", "v")}
+    want = {}
+    for x in ("k", "v"):
+        was = b.r[x + "_scale"][:, :, 1].copy()
+        rows = new[x].double().cpu().numpy().transpose(0, 2, 1, 3)
+        need = np.vectorize(ref.scale_of)(np.abs(rows).max((2, 3)))
+        now = np.maximum(np.exp2(np.ceil(np.log2(was))), need)
+        b.r[x][:, :, 16:held] = ref.e4m3(b.r[x][:, :, 16:held] * (was / now)[:, :, None, None])
+        b.r[x][:, :, held:held + 3] = ref.e4m3(rows / now[:, :, None, None])
+        b.r[x + "_scale"][:, :, 1] = now
+        want[x] = before[x][:, :, 16:held] * was[:, :, None, None], rows
+    xkv.xkv_kv8_append(b.p, b.c, b.dev_lens(), new["k"].flatten(2), new["v"].flatten(2))
+    b.lens = [held + 3] * B
+    b.check()
+    for x in ("k", "v"):  # each within half a step of what it stands for, of a number or of the least one
+        now = b.r[x + "_scale"][:, :, 1][:, :, None, None]
+        for got, true in zip((b.r[x][:, :, 16:held] * now, b.r[x][:, :, held:held + 3] * now), want[x]):
+            assert (np.abs(got - true) <= np.abs(true) * 2.0 ** -4 + now * 2.0 ** -10).all()
+
+
 def test_append_reads_views_and_writes_only_its_rows(xkv):
     B, H, hd, block, cap, n = 2, 2, 64, 16, 96, 21
     g = torch.Generator().manual_seed(3)
