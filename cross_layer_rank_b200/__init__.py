@@ -570,9 +570,11 @@ def xkv_kv8_append(p: KV8Params, cache: KV8Cache, lens, k_new, v_new, counts=Non
     if len(shape) != 3 or v_new.shape != shape or v_new.dtype != dtype or shape[0] != p.batch or \
             shape[2] != p.n_kv_heads * p.head_dim:
         raise ValueError("k_new and v_new are [B][n][Hkv hd] of one dtype")
-    if strides[2] != 1 or v_new.stride() != strides:
-        raise ValueError("k_new and v_new need contiguous rows and the same strides")
     # a stride over one row or one sequence is not used, and torch leaves it open
+    other = v_new.stride()
+    if strides[2] != 1 or other[2] != 1 or (strides[1] != other[1] and shape[1] > 1) or \
+            (strides[0] != other[0] and shape[0] > 1):
+        raise ValueError("k_new and v_new need contiguous rows and the same strides")
     _check(lib.xkv_kv8_append(p, cache.pointers, _lens_ptr(p, lens), _lens_ptr(p, counts), shape[1],
                               dtype_code(dtype), k_new.data_ptr(), v_new.data_ptr(),
                               strides[1] if shape[1] > 1 else shape[2], strides[0] if shape[0] > 1 else 0,

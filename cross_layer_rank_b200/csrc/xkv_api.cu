@@ -734,8 +734,9 @@ xkv_status xkv_kv8_append(const xkv_kv8_params* p, const xkv_kv8_cache* cache, c
   if (s != XKV_OK) return s;
   if (dtype != XKV_F32 && dtype != XKV_BF16) return XKV_ERR_INVALID_ARG;
   const int per16 = dtype == XKV_BF16 ? 8 : 4;
-  if (!lens || !aligned4(lens) || !aligned4(counts) || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) ||
-      n_new < 0 || n_new > p->capacity || row_stride < static_cast<int64_t>(p->n_kv_heads) * p->head_dim ||
+  // no rows need no address (an empty tensor has none)
+  if (!lens || !aligned4(lens) || !aligned4(counts) || (n_new != 0 && (!k_new || !v_new)) || !aligned16(k_new) ||
+      !aligned16(v_new) || n_new < 0 || n_new > p->capacity || row_stride < static_cast<int64_t>(p->n_kv_heads) * p->head_dim ||
       row_stride % per16 != 0 || batch_stride < 0 || batch_stride % per16 != 0)
     return XKV_ERR_INVALID_ARG;
   if (n_new == 0) return XKV_OK;

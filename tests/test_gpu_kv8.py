@@ -203,6 +203,32 @@ def test_append_reads_views_and_writes_only_its_rows(xkv):
     b.check()
 
 
+def test_append_of_no_rows_and_of_strides_that_nothing_uses(xkv):
+    B, H, hd, block = 1, 2, 64, 16
+    b, g = _fill(xkv, B, H, hd, block, 64, [21])
+    none = torch.empty((B, 0, H * hd), dtype=torch.bfloat16, device="cuda")
+    xkv.xkv_kv8_append(b.p, b.c, b.dev_lens(), none, none)
+    b.check()
+    k = _rows(g, B, 1, H, hd, "bf16")  # one row of one sequence, its value a view into a projection
+    qkv = _rows(g, B, 1, 3 * H, hd, "bf16")
+    v = qkv.flatten(2)[..., 2 * H * hd:]
+    assert v.stride() != k.flatten(2).stride() and v.stride(2) == 1
+    xkv.xkv_kv8_append(b.p, b.c, b.dev_lens(), k.flatten(2), v)
+    ref.append(b.r, block, b.lens, k.double().cpu().numpy(), v.double().cpu().numpy().reshape(B, 1, H, hd), [1])
+    b.lens = [22]
+    b.check()
+    k, v = _rows(g, B, 5, H, hd, "bf16").flatten(2), _rows(g, 2, 5, H, hd, "bf16").flatten(2)
+    wide = torch.empty((1, 9, H * hd), dtype=torch.bfloat16, device="cuda")[:, :5]  # another stride between sequences
+    wide.copy_(v[:1])
+    xkv.xkv_kv8_append(b.p, b.c, b.dev_lens(), k, wide)
+    ref.append(b.r, block, b.lens, k.double().cpu().numpy().reshape(B, 5, H, hd),
+               v[:1].double().cpu().numpy().reshape(B, 5, H, hd), [5])
+    b.check()
+    with pytest.raises(ValueError):  # rows of unlike strides
+        xkv.xkv_kv8_append(b.p, b.c, b.dev_lens(), k, torch.empty((1, 5, 2 * H * hd), dtype=torch.bfloat16,
+                                                                  device="cuda")[..., :H * hd])
+
+
 def test_append_past_the_capacity_and_bad_lengths(xkv):
     g = torch.Generator().manual_seed(4)
     b = Both(xkv, 3, 1, 32, 8, 32)

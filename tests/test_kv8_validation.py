@@ -76,6 +76,14 @@ def test_append_arguments(xkv):
         assert call(**bad) == xkv.XKV_ERR_INVALID_ARG, bad
 
 
+def test_append_of_no_rows_needs_no_address(xkv):
+    # an empty tensor has none
+    f = xkv.lib.xkv_kv8_append
+    assert f(_p(xkv), _c(xkv), FAKE, None, 0, xkv.XKV_BF16, None, None, 128, 0, None) == xkv.XKV_OK
+    assert f(_p(xkv), _c(xkv), None, None, 0, xkv.XKV_BF16, None, None, 128, 0, None) == xkv.XKV_ERR_INVALID_ARG
+    assert f(_p(xkv), _c(xkv), FAKE, None, 1, xkv.XKV_BF16, FAKE, None, 128, 0, None) == xkv.XKV_ERR_INVALID_ARG
+
+
 def test_attention_and_eviction_arguments(xkv):
     p, c, inv = _p(xkv), _c(xkv), xkv.XKV_ERR_INVALID_ARG
     f = xkv.lib.xkv_kv8_attention_decode
