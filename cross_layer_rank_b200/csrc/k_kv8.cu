@@ -216,8 +216,6 @@ __global__ void __launch_bounds__(append_threads(W)) kv8_append_kernel(const App
 
 // ------------------------------------------------------------- attention
 struct AttendArgs {
-  const uint8_t* k;
-  const uint8_t* v;
   const float* k_scale;
   const float* v_scale;
   const void* q;
@@ -1701,8 +1699,6 @@ xkv_status kv8_attend_launch(const xkv_kv8_params* p, const xkv_kv8_cache* c, co
                              xkv_dtype dt, const void* q, float* out, int accumulate, const KV8Plan& plan, void* ws,
                              cudaStream_t st) {
   AttendArgs a{};
-  a.k = static_cast<const uint8_t*>(c->k);
-  a.v = static_cast<const uint8_t*>(c->v);
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;
   a.q = q;
