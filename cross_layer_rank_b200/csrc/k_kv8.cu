@@ -105,7 +105,11 @@ struct Raw16<float> {
 // take 8.7 us, and took 20 with a CTA each.
 // Bound by HBM for prompts: four of 64K tokens, 8 heads of 128 (1.61 GB), take
 // 238 to 265 us as the card warms up, 6.8 to 6.1 TB/s, a plain copy's rate; one
-// token for 32 sequences takes 2.1 us, a launch.
+// token for 32 sequences takes 2.1 us, a launch.  A part-filled block whose scale
+// grows costs its own codes a read and a write by the same warps, a vector a lane
+// at a time: one token for 32 sequences, 8 heads of 128, blocks of 64, every
+// block growing, takes 1.1 us more with blocks half full and 2.8 with full ones;
+// blocks of 128 x 256, 4.1 and 8.6.
 constexpr int append_threads(int W) { return W == 8 ? 256 : 128; }
 
 template <typename T, int NV, int W>
@@ -239,8 +243,8 @@ __host__ __device__ inline int sub_rows(int block) { return block < 32 ? block :
 // Units' tiles stand in one line (sequence, head, tile), and CTA c of n takes a
 // contiguous share of it: ragged lengths need no more CTAs than the card runs.
 // A unit of nt tiles takes nt + 1 places, the last one empty: starting and
-// ending a unit costs a CTA about as much as a tile (2.2 and 4.4 thousand clocks
-// for a tile of a long unit and a unit of one tile, 8 query heads of 64 columns;
+// ending a unit costs a CTA about as much as a tile (8 query heads of 64 columns:
+// 0.9 and 0.8 thousand clocks of each warpgroup, and a tile 2.8 of one of the two;
 // 48 sequences of 1 to 8192 tokens took 32 us by tiles alone).
 struct Share {
   int lo, hi;
@@ -503,11 +507,16 @@ __device__ __forceinline__ void group_sums(const float* p, int sub, F f) {
 // the MMA (0 * NaN).
 // Bound by HBM where units are long: 4 sequences of 64K tokens, 8 KV heads of 128
 // with 4 query heads each, take 90 us with the join, 6.0 TB/s (537 MB, all of them
-// read once: 537.3 MB of DRAM reads; the tensor pipe is 8 % busy).  Otherwise by
-// the chain of a tile's steps, about 2500 clocks with 8 query heads, of which two
-// warpgroups have one each in flight: 48 sequences of 1 to 8192 tokens, 4 x 8 heads
-// of 64, take 23 us (23 MB).  Three warpgroups (512 threads, registers moved to
-// them) spilled: 72 us instead of 53 for two sequences of 128K tokens, 4 x 7 heads.
+// read once: 537.3 MB of DRAM reads; the tensor pipe is 6.6 % busy).  Otherwise by
+// the chain of a tile's steps, 2600 to 2850 clocks with 8 query heads, of which two
+// warpgroups have one each in flight, and which waits for S for 160 to 220 of them:
+// two sequences of 128K tokens, 4 x 7 heads, take 51 us (268 MB), 41 of them 28
+// tiles of each warpgroup; 48 sequences of 1 to 8192 tokens, 4 x 8 heads of 64, take
+// 23 us (23 MB), where a CTA of eleven tiles runs for 13 us and the slowest, of six
+// short units, for 18.  Three warpgroups (512 threads, registers moved to them)
+// spilled: 72 us instead of 53 for the two long sequences.
+// Registers: 8 query heads of 256 columns and 16 of either width are at the limit of
+// 168 a thread and spill 36 to 84 bytes.
 template <typename T, int GQ, int HDA>
 __global__ void __launch_bounds__(kAttendThreads, 1)
 kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -1334,7 +1343,8 @@ __device__ __forceinline__ int find_word(const int* pref, int lo, int hi, int r)
 // 18 us: 5 of selection, a chain of block-wide steps, 8 of moves (9 TB/s read and
 // written, the writes into L2) and the rest launch, loads and prefix sums.  Sixty
 // units cut from 5113 blocks of 8 x 48 to 2556 (59 MB to move) take 57 us, 178 with
-// one move at a time: the selection is 9 of them.
+// one move at a time: the selection is 9 of them (that instantiation spills 20
+// bytes at its 80 registers, three CTAs an SM).
 template <bool kGroups>
 __global__ void __launch_bounds__(kEvictThreads, 3) kv8_evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_dyn[];

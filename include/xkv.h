@@ -440,7 +440,9 @@ XKV_API xkv_status xkv_dense_attention_decode(const xkv_dense_params* p, const v
  * Lengths are on the device: lens [B] int32 holds the tokens of every sequence,
  * the same for all its heads; the calls read it and never write it, so that one
  * array serves every layer and the caller advances it once a step.  What stands
- * behind a sequence's last row is neither read nor written.  A length outside
+ * behind a sequence's last row never reaches a result: attention may read it
+ * (tiles of 128 rows, whole ones), eviction moves whole blocks, the unused rows of
+ * the newest one with them, and nothing else is written there.  A length outside
  * [0, capacity] is taken as the nearer end and XKV_ERR_INVALID_ARG is recorded
  * in the device status word.
  * head_dim is a multiple of 16 up to 256; block is 8, 16, 32, 64 or 128 and
@@ -468,12 +470,11 @@ typedef struct xkv_kv8_cache {
  * for the scale.  A block that held rows before keeps the larger of its scale
  * and the new rows' one; when that makes its scale grow, its codes are rounded
  * once more on the new scale.  A scale of the block that is no power of two (a
- * cache filled by other means; attention takes any positive scale) is raised to
- * the next one in the same way, and one above 2^120 becomes 2^120.  A block
- * opened by the call gets weight 0 and the
- * number after the last block's.  Rows past the capacity are dropped and
- * XKV_ERR_INVALID_ARG is recorded in the device status word.  lens is not
- * advanced. */
+ * cache filled by other means; attention takes any positive normal one) is raised
+ * to the next one in the same way, and one above 2^120 becomes 2^120.  A block
+ * opened by the call gets weight 0 and the number after the last block's.  Rows
+ * past the capacity are dropped and XKV_ERR_INVALID_ARG is recorded in the device
+ * status word.  lens is not advanced. */
 XKV_API xkv_status xkv_kv8_append(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
                                   const int32_t* counts, int64_t n_new, xkv_dtype dtype, const void* k_new,
                                   const void* v_new, int64_t row_stride, int64_t batch_stride, void* stream);
@@ -484,7 +485,19 @@ XKV_API xkv_status xkv_kv8_append(const xkv_kv8_params* p, const xkv_kv8_cache* 
  *         (else XKV_ERR_UNSUPPORTED).   out : [B][Hq][hd] f32.
  * With accumulate, every block's weight grows by the softmax probabilities of
  * its rows, summed over the KV head's query heads.  A step gives the same bits
- * whenever it is repeated. */
+ * whenever it is repeated.  A NaN among a head's logits, its query's not finite
+ * entries among them, makes its outputs NaN, and a NaN value its column.
+ *   Logits, softmax and sums are f32.  Two operands are cut into parts that the
+ * tensor cores take beside the codes, and what is far below their largest ends
+ * there: a query keeps all bits of entries down to 2^-22 (bf16) or 2^-14 (f32) of
+ * its head's largest and the rest to 2^-30 or 2^-38 of it; a row's probability
+ * times its block's value scale is held to 2^-31 of the largest of its 128-row
+ * tile (rows 0-127, 128-255, ... of the cache), or, for more than 8 query heads a
+ * KV head of more than 128 columns, to 24 bits and 2^-37 of it.  So an output
+ * column that lives on rows whose products are 2^-x of their tile's largest (an
+ * outlier makes its block's value scale 2^x times the others', or a sink has
+ * almost all probability and no value) is exact to about 2^(x - 31) of itself
+ * where that is above f32's own error. */
 XKV_API xkv_status xkv_kv8_workspace_size(const xkv_kv8_params* p, int n_q_heads, size_t* bytes);
 XKV_API xkv_status xkv_kv8_attention_decode(const xkv_kv8_params* p, const xkv_kv8_cache* cache, const int32_t* lens,
                                             int n_q_heads, xkv_dtype dtype, const void* q, float* out,
