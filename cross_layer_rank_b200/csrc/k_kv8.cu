@@ -1192,7 +1192,14 @@ __global__ void __launch_bounds__(kCombineThreads, 4) kv8_combine_kernel(const A
         for (int j = 0; j < kHeld; ++j) {
           const int k = from + j * wph;
           const float f = k < slots ? s_f[slot][k] : NAN;
-          if (isnan(f)) continue;  // a slot without rows holds anything; one of factor 0 may hold a NaN
+          if (isnan(f)) continue;  // a slot without rows holds anything
+          if (f == 0.f) {          // of a slot that weighs nothing, NaN alone: values near f32's largest may sum to inf
+            auto nan_only = [](float4& t) {
+              t = make_float4(isnan(t.x) ? t.x : 0.f, isnan(t.y) ? t.y : 0.f, isnan(t.z) ? t.z : 0.f, isnan(t.w) ? t.w : 0.f);
+            };
+            nan_only(v[j]);
+            nan_only(z[j]);
+          }
           add(x, f, v[j]);
           if (hi) add(y, f, z[j]);
         }

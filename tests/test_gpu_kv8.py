@@ -447,6 +447,21 @@ def test_nan_values_of_rows_without_weight(xkv, gq, hd, block, n, row):
     assert torch.equal(out, good)
 
 
+def test_largest_values_of_rows_without_weight(xkv):
+    # a tile whose values sum past f32's largest, and whose probabilities are all 0 in f32: nothing of it is left
+    n, hd, gq = 200, 64, 4
+    b, g = _fill(xkv, 1, 1, hd, 8, n, [n])
+    b.c.k.view(torch.uint8).zero_()
+    b.c.k[:, :, :8] = torch.full((1, 1, 8, hd), 8.0).to(F8).cuda()
+    b.c.k_scale.fill_(1.0)
+    q = torch.full((1, gq, hd), 100.0 / hd ** 0.5, dtype=torch.float32, device="cuda")
+    good = _attend(b, q)
+    b.c.v[:, :, 128:] = torch.full((1, 1, n - 128, hd), 448.0).to(F8).cuda()
+    b.c.v_scale[:, :, 16:] = 2.0 ** 119
+    out = _attend(b, q)
+    assert out.isfinite().all() and torch.equal(out, good)
+
+
 def test_attention_writes_only_its_outputs(xkv):
     counts = [77, 0, 300]
     b, g = _fill(xkv, 3, 2, 80, 16, 304, counts)
